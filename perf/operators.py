@@ -313,7 +313,7 @@ def _handle(s):
         h = mixers.PagedKV(c["heads"], c["kv_heads"], c["dim"], c["page"], kv_fmt=c["fmt"],
                            buffers=(s["k_codes"], s["v_codes"], s["k_scale"], s["v_scale"]))
         s["batch"] = h.batch(s["q_start"], s["kv_len"], s["table"], n_tokens=T, max_new=c["max_new"])
-        s["ws"] = h.workspace(B)
+        s["ws"] = h.workspace()
         if c["op"] == "attend":
             s["out"] = torch.empty_like(s["q"])
             s["lse"] = torch.empty(T, c["heads"], device=DEV)
