@@ -297,6 +297,168 @@ LMOE_API int lmoe_dproj_ablation(const lmoe_cfg* cfg, const void* x, const void*
 LMOE_API int lmoe_route_noalloc(const lmoe_cfg* cfg, const void* x, const void* router_w, const float* router_b,
                                 int T, int32_t* topk_idx, float* topk_w, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Token mixers: the two mixers that stand before the block in the hybrid
+ * Edge0 layers (model page, "Model profile": 36 gated-delta layers and 12
+ * attention layers, keys and values cached in 8 bits).  Their projections
+ * are the caller's; the operators take q, k, v rows.  The conventions above
+ * hold; ws is a workspace of the operator's own *_workspace_bytes, whose
+ * first word is the status word of lmoe_last_device_status.
+ *
+ * The paged cache holds, per page and key head, page_size rows of head_dim
+ * codes and one fp32 scale per row, keys and values alike:
+ *   k, v              [n_pages][n_kv_heads][page_size][head_dim] codes
+ *   k_scale, v_scale  [n_pages][n_kv_heads][page_size] fp32
+ *   value = code * scale.  With a = max|x| of a row:
+ *     LMOE_KV_INT8: scale = a / 127, code = 127 x / a to the nearest, ties
+ *                   to even, signed 8-bit
+ *     LMOE_KV_E4M3: scale = a / 448, code = 448 x / a to the nearest E4M3
+ *                   value, ties to even
+ *   Scales are fp32 divisions; the codes are those of exact arithmetic.  A
+ *   row with a < 2^-100 is stored as zeros with scale 1, a row with an
+ *   infinity or a NaN as zeros with a NaN scale (every query that reads it
+ *   then gets NaN), which is also reported.
+ *
+ * A batch describes the new tokens of n_seqs sequences: rows
+ * q_start[s] .. q_start[s+1] - 1 of the token arrays are the last tokens of
+ * sequence s, whose cache holds kv_len[s] tokens with them.  Token i of
+ * sequence s (i from 0) has position kv_len[s] - n_s + i; position p is
+ * row p % page_size of page page_table[s][p / page_size].  Rows from
+ * q_start[n_seqs] on belong to no sequence and are left as they were, so a
+ * batch may be padded.  The lengths are read on the device: a captured
+ * graph may be replayed with other lengths under the same n_seqs, n_tokens
+ * and max_new.  Sequences may share pages that are only read; two rows of
+ * one append that name the same place leave either one there.
+ *   Checked on the device, reported as LMOE_ERR_DEVICE_CHECK: a sequence
+ *   with n_s < 0, n_s > max_new, rows outside [0, n_tokens), kv_len < 0 or
+ *   beyond its page table is left out whole (its rows stay as they were); a
+ *   page outside [0, n_pages) is neither read nor written, its keys count
+ *   as masked, and rows read from it are zeros. */
+typedef enum { LMOE_KV_INT8 = 0, LMOE_KV_E4M3 = 1 } lmoe_kv_fmt;
+
+typedef struct {
+    int n_heads;       /* query heads, a multiple of n_kv_heads */
+    int n_kv_heads;    /* key / value heads; query head j reads key head j / (n_heads / n_kv_heads) */
+    int head_dim;      /* 64, 128 or 256 */
+    int page_size;     /* tokens a page: a power of two, 16 to 1024 */
+    int kv_fmt;        /* lmoe_kv_fmt */
+} lmoe_attn_cfg;
+
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int n_pages;
+} lmoe_kv_cache;
+
+typedef struct {
+    const int32_t* q_start;      /* [n_seqs + 1], device */
+    const int32_t* kv_len;       /* [n_seqs], device */
+    const int32_t* page_table;   /* [n_seqs][pages_per_seq], device; entries past kv_len are not read */
+    int n_seqs;
+    int pages_per_seq;
+    int n_tokens;                /* rows of the token arrays */
+    int max_new;                 /* no sequence has more new tokens than this */
+} lmoe_kv_batch;
+
+/* LMOE_OK if the shape is supported: the limits at the fields, n_heads and
+ * n_kv_heads up to 1024. */
+LMOE_API int lmoe_attn_cfg_check(const lmoe_attn_cfg* cfg);
+
+/* Bytes of the workspace of lmoe_kv_append, lmoe_kv_read and lmoe_attend for
+ * batches of any size (the lengths do not enter).  0 if the configuration
+ * is unsupported. */
+LMOE_API size_t lmoe_attn_workspace_bytes(const lmoe_attn_cfg* cfg);
+
+/* Quantise the new tokens' keys and values into the cache.
+ * k, v: bf16, row r at k + r * k_stride elements (strides multiples of 8, at
+ * least n_kv_heads * head_dim; slices of a fused projection's rows serve),
+ * its heads one after the other.  Tokens at negative positions
+ * (kv_len < n_s) are not stored.
+ * Errors: LMOE_ERR_ARG, _UNSUPPORTED, _WORKSPACE; n_tokens = 0 or
+ * n_seqs = 0 launches nothing. */
+LMOE_API int lmoe_kv_append(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_kv_batch* batch, const void* k,
+                            const void* v, size_t k_stride, size_t v_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* The mirror of lmoe_kv_append: the cached rows of the batch's tokens (the
+ * last n_s of each sequence; n_s = kv_len reads a whole context) as bf16
+ * values.  k, v as there, written; tokens at negative positions are zeros.
+ * Errors as lmoe_kv_append. */
+LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_kv_batch* batch, void* k, void* v,
+                          size_t k_stride, size_t v_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the batch's tokens over their sequences' caches (which hold
+ * the tokens' own keys already):
+ *   out[i] = sum_j softmax_j(softmax_scale * q_i . k_j) v_j
+ * over the positions j < kv_len with, if causal, j <= i's position and, if
+ * window > 0 (causal only), j > i's position - window.  causal = 0 serves an
+ * encoder's states of another length.  A row without any key gets zeros.
+ *   q    bf16, row r at q + r * q_stride elements (a multiple of 8, at least
+ *        n_heads * head_dim)
+ *   out  bf16 [n_tokens][n_heads][head_dim]
+ *   lse  fp32 [n_tokens][n_heads] or NULL: log of the sum of exponentials
+ *        (-inf for a row without keys), for joining parts of a context
+ * Products are of the bf16 queries and the stored codes as fp16, exact, with
+ * fp32 sums; the probabilities (times the value's scale) are rounded to
+ * fp16.  Results do not depend on timing.
+ * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that
+ * is not finite), _UNSUPPORTED, _WORKSPACE; n_tokens = 0 or n_seqs = 0
+ * launches nothing. */
+LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_kv_batch* batch, const void* q,
+                         size_t q_stride, float softmax_scale, int causal, int window, void* out, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* The gated delta rule over the new tokens of n_seqs sequences, each with a
+ * state S [head_k][head_v] per head:
+ *   S <- exp(log_decay) S;  S <- S + beta k (v - k^T S);  out = scale S^T q
+ * A token step of a few tokens runs the recurrence, longer sequences its
+ * chunked form; both hold the state and every sum that enters it in fp32. */
+typedef struct {
+    int n_heads;       /* heads of v, the gates and the state: a multiple of n_qk_heads */
+    int n_qk_heads;    /* heads of q and k; head j uses q, k head j / (n_heads / n_qk_heads) */
+    int head_k;        /* 64 or 128 */
+    int head_v;        /* 64 or 128 */
+    int l2norm;        /* nonzero: q and k rows are divided by sqrt(sum of squares + 1e-6) first */
+} lmoe_delta_cfg;
+
+typedef struct {
+    const int32_t* q_start;      /* [n_seqs + 1], device: rows of each sequence, as in lmoe_kv_batch */
+    const int32_t* src;          /* [n_seqs], device: the state a sequence starts from; -1: zeros */
+    const int32_t* dst;          /* [n_seqs], device: where its last state goes (src's place, or another); -1: nowhere */
+    int n_seqs;
+    int n_states;
+    int n_tokens;
+    int max_new;
+} lmoe_delta_batch;
+
+/* LMOE_OK if the shape is supported: the limits at the fields, heads up to
+ * 1024. */
+LMOE_API int lmoe_delta_cfg_check(const lmoe_delta_cfg* cfg);
+
+/* Bytes of the workspace of lmoe_delta_rule for batches of up to n_tokens
+ * tokens of n_seqs sequences with up to max_new tokens each.  0 if
+ * unsupported. */
+LMOE_API size_t lmoe_delta_workspace_bytes(const lmoe_delta_cfg* cfg, int n_tokens, int n_seqs, int max_new);
+
+/*   q, k   bf16 rows of n_qk_heads * head_k, v bf16 rows of n_heads * head_v,
+ *          at strides of q_stride, k_stride, v_stride elements (multiples
+ *          of 8)
+ *   log_decay, beta   fp32 [n_tokens][n_heads]; log_decay <= 0 (-inf forgets)
+ *   states fp32 [n_states][n_heads][head_k][head_v], read at src and written
+ *          at dst; one batch must not name a place as dst that another of
+ *          its sequences names as src or dst
+ *   out    bf16 [n_tokens][n_heads][head_v]
+ * A sequence without new tokens copies its state.  Checked on the device
+ * (LMOE_ERR_DEVICE_CHECK, the sequence is left out): rows as in
+ * lmoe_kv_batch, src or dst outside [-1, n_states).
+ * Errors: LMOE_ERR_ARG, _UNSUPPORTED, _WORKSPACE; n_seqs = 0 launches
+ * nothing. */
+LMOE_API int lmoe_delta_rule(const lmoe_delta_cfg* cfg, const lmoe_delta_batch* batch, const void* q, const void* k,
+                             const void* v, size_t q_stride, size_t k_stride, size_t v_stride, const float* log_decay,
+                             const float* beta, float scale, float* states, void* out, void* ws, size_t ws_bytes,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,12 +29,16 @@ LMOE_EXPERTS_NVFP4 = 0
 LMOE_EXPERTS_Q3K = 1
 LMOE_ACT_FP16 = 0
 LMOE_ACT_NVFP4 = 1
+LMOE_KV_INT8 = 0
+LMOE_KV_E4M3 = 1
 
 # every symbol include/lmoe.h declares
 EXPORTS = ("lmoe_cfg_check", "lmoe_expert_record_bytes", "lmoe_du_bytes", "lmoe_workspace_bytes", "lmoe_route",
            "lmoe_forward", "lmoe_forward_ex", "lmoe_forward_host", "lmoe_stack_forward", "lmoe_last_device_status",
            "lmoe_status_str", "lmoe_debug_decode", "lmoe_debug_act_quant", "lmoe_profile_stage_events",
-           "lmoe_route_noalloc", "lmoe_dproj_ablation")
+           "lmoe_route_noalloc", "lmoe_dproj_ablation", "lmoe_attn_cfg_check", "lmoe_attn_workspace_bytes",
+           "lmoe_kv_append", "lmoe_kv_read", "lmoe_attend", "lmoe_delta_cfg_check", "lmoe_delta_workspace_bytes",
+           "lmoe_delta_rule")
 
 
 class LmoeError(RuntimeError):
@@ -56,6 +60,28 @@ class lmoe_layer(ctypes.Structure):
     _fields_ = [("router_w", ctypes.c_void_p), ("router_b", ctypes.c_void_p), ("expert_group", ctypes.c_void_p),
                 ("D", ctypes.c_void_p), ("U", ctypes.c_void_p), ("experts", ctypes.c_void_p),
                 ("shared", lmoe_shared), ("norm_gamma", ctypes.c_void_p)]
+
+
+class lmoe_attn_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_heads", "n_kv_heads", "head_dim", "page_size", "kv_fmt")]
+
+
+class lmoe_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [("n_pages", ctypes.c_int)]
+
+
+class lmoe_kv_batch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q_start", "kv_len", "page_table")]
+                + [(n, ctypes.c_int) for n in ("n_seqs", "pages_per_seq", "n_tokens", "max_new")])
+
+
+class lmoe_delta_cfg(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_heads", "n_qk_heads", "head_k", "head_v", "l2norm")]
+
+
+class lmoe_delta_batch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q_start", "src", "dst")]
+                + [(n, ctypes.c_int) for n in ("n_seqs", "n_states", "n_tokens", "max_new")])
 
 
 _lib = None
@@ -102,6 +128,23 @@ def lib() -> ctypes.CDLL:
         L.lmoe_route_noalloc.restype = i32
         L.lmoe_dproj_ablation.argtypes = [cfgp, vp, vp, i32, ctypes.c_uint32, vp, i32, vp, sz, vp]
         L.lmoe_dproj_ablation.restype = i32
+        atp, kvp, kbp = (ctypes.POINTER(c) for c in (lmoe_attn_cfg, lmoe_kv_cache, lmoe_kv_batch))
+        dcp, dbp = ctypes.POINTER(lmoe_delta_cfg), ctypes.POINTER(lmoe_delta_batch)
+        L.lmoe_attn_cfg_check.argtypes = [atp]
+        L.lmoe_attn_cfg_check.restype = i32
+        L.lmoe_attn_workspace_bytes.argtypes = [atp]
+        L.lmoe_attn_workspace_bytes.restype = sz
+        for n in ("lmoe_kv_append", "lmoe_kv_read"):
+            getattr(L, n).argtypes = [atp, kvp, kbp, vp, vp, sz, sz, vp, sz, vp]
+            getattr(L, n).restype = i32
+        L.lmoe_attend.argtypes = [atp, kvp, kbp, vp, sz, f32, i32, i32, vp, vp, vp, sz, vp]
+        L.lmoe_attend.restype = i32
+        L.lmoe_delta_cfg_check.argtypes = [dcp]
+        L.lmoe_delta_cfg_check.restype = i32
+        L.lmoe_delta_workspace_bytes.argtypes = [dcp, i32, i32, i32]
+        L.lmoe_delta_workspace_bytes.restype = sz
+        L.lmoe_delta_rule.argtypes = [dcp, dbp, vp, vp, vp, sz, sz, sz, vp, vp, f32, vp, vp, vp, sz, vp]
+        L.lmoe_delta_rule.restype = i32
         _lib = L
     return _lib
 
@@ -252,3 +295,45 @@ def lmoe_dproj_ablation(cfg, x, D, act_fmt, group_mask, h, T, ws, stream=None):
     return _check(lib().lmoe_dproj_ablation(ctypes.byref(cfg), _ptr(x), _ptr(D), int(act_fmt), int(group_mask),
                                             _ptr(h), T, _ptr(ws), _nbytes(ws), _stream(stream)),
                   "lmoe_dproj_ablation")
+
+
+# ----------------------------------------------------------------------------
+# token mixers (strides in elements; the structures hold device addresses)
+# ----------------------------------------------------------------------------
+
+def lmoe_attn_cfg_check(cfg: lmoe_attn_cfg) -> int:
+    return lib().lmoe_attn_cfg_check(ctypes.byref(cfg))
+
+
+def lmoe_attn_workspace_bytes(cfg: lmoe_attn_cfg) -> int:
+    return lib().lmoe_attn_workspace_bytes(ctypes.byref(cfg))
+
+
+def lmoe_kv_append(cfg, cache, batch, k, v, k_stride, v_stride, ws, stream=None):
+    return _check(lib().lmoe_kv_append(cfg, cache, batch, _ptr(k), _ptr(v), k_stride, v_stride, _ptr(ws), _nbytes(ws),
+                                       _stream(stream)), "lmoe_kv_append")
+
+
+def lmoe_kv_read(cfg, cache, batch, k, v, k_stride, v_stride, ws, stream=None):
+    return _check(lib().lmoe_kv_read(cfg, cache, batch, _ptr(k), _ptr(v), k_stride, v_stride, _ptr(ws), _nbytes(ws),
+                                     _stream(stream)), "lmoe_kv_read")
+
+
+def lmoe_attend(cfg, cache, batch, q, q_stride, softmax_scale, causal, window, out, lse, ws, stream=None):
+    return _check(lib().lmoe_attend(cfg, cache, batch, _ptr(q), q_stride, softmax_scale, int(causal), window, _ptr(out),
+                                    _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)), "lmoe_attend")
+
+
+def lmoe_delta_cfg_check(cfg: lmoe_delta_cfg) -> int:
+    return lib().lmoe_delta_cfg_check(ctypes.byref(cfg))
+
+
+def lmoe_delta_workspace_bytes(cfg: lmoe_delta_cfg, n_tokens: int, n_seqs: int, max_new: int) -> int:
+    return lib().lmoe_delta_workspace_bytes(ctypes.byref(cfg), n_tokens, n_seqs, max_new)
+
+
+def lmoe_delta_rule(cfg, batch, q, k, v, q_stride, k_stride, v_stride, log_decay, beta, scale, states, out, ws,
+                    stream=None):
+    return _check(lib().lmoe_delta_rule(cfg, batch, _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
+                                        _ptr(log_decay), _ptr(beta), scale, _ptr(states), _ptr(out), _ptr(ws),
+                                        _nbytes(ws), _stream(stream)), "lmoe_delta_rule")

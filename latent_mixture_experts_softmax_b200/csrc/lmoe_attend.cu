@@ -1,0 +1,744 @@
+// Attention of new tokens over the 8-bit paged cache: the kernel for few
+// query rows per key head (decode steps and verify windows), and the kernel
+// that joins results cut between CTAs.
+//
+// Mathematics.  For one key head the query rows are the pairs (new token,
+// query head of its group); with codes c_j and scales a_j (keys), b_j
+// (values),
+//   t_j = scale log2(e) a_j (q . ck_j) + log2(b_j),   p_j = 2^(t_j - m),
+//   out = sum_j p_j cv_j / sum_j p_j (1 / b_j).
+// Folding the value's scale into the exponent keeps the second product in
+// fp16 whatever the scales are: p is at most 2^8 (below) and the codes are
+// exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
+// that of p to fp16 (half a step, 2^-12).  Queries are scaled by a power of
+// two per row into the fp16 range, which is exact; sums are fp32.
+//
+// What bounds it: the bytes of the codes, each read once.  The products run
+// on mma.sync m16n8k16 with the tokens as M (S^T = K Q^T) and the query rows
+// as N, so 8 rows cost one instruction per 16 tokens and 16 columns, and
+// neither product needs a transposed copy of the codes: both sums run over
+// permuted index orders that make a lane's operand bytes contiguous in the
+// stored rows (16-byte loads straight to registers, converted there).
+//
+// Split: the work of all (sequence, key head, row tile) items is laid out on
+// one line in units of 128 tokens and cut into equal pieces, one per CTA
+// whatever the lengths; the 8 warps of a CTA take 16-token steps in turn and
+// join their results through shared memory.  An item cut between CTAs leaves
+// its parts in the workspace for k_attend_join, which adds them in order.
+
+#include "lmoe_mixers.cuh"
+#include "lmoe_sm100.cuh"
+
+namespace lmoe {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxRows = 32;        // query rows of one item
+constexpr int kMaxCtas = 2 * kSms;
+
+// ---------------------------------------------------------------------------
+// the line of work units
+// ---------------------------------------------------------------------------
+
+struct Plan {
+    int rows;          // query rows of a row tile
+    int groups;        // 16-token steps of a unit
+};
+
+struct Tile {
+    int step0, step1;  // 16-token steps the row tile reads
+    int units;         // at least one, so that empty tiles are written too
+};
+
+__device__ __forceinline__ Tile tile_of(const AttendParams& p, const Plan& pl, const SeqRows& s, int rt) {
+    const int r0 = rt * pl.rows, r1 = min(r0 + pl.rows, s.n * p.G);
+    const int first = s.kv - s.n;
+    int lo = 0, hi = s.kv;
+    if (p.causal) {
+        hi = min(hi, first + (r1 - 1) / p.G + 1);
+        if (p.window) lo = max(0, first + r0 / p.G - p.window + 1);
+    }
+    hi = max(hi, lo);
+    Tile t;
+    t.step0 = lo >> 4;
+    t.step1 = max(t.step0, hi > lo ? (hi + 15) >> 4 : t.step0);
+    t.units = max(1, (t.step1 - t.step0 + pl.groups - 1) / pl.groups);
+    return t;
+}
+
+__device__ __forceinline__ int n_row_tiles(const AttendParams& p, const Plan& pl, const SeqRows& s) {
+    return s.n <= 0 ? 0 : (int)(((long long)s.n * p.G + pl.rows - 1) / pl.rows);
+}
+
+// Units of one head of a sequence.
+__device__ __forceinline__ long long head_units(const AttendParams& p, const Plan& pl, const SeqRows& s) {
+    long long u = 0;
+    for (int rt = 0, n = n_row_tiles(p, pl, s); rt < n; ++rt) u += tile_of(p, pl, s, rt).units;
+    return u;
+}
+
+struct Line {
+    long long total, chunk;   // units, and units per CTA
+    int seq;                  // the sequence holding unit x, and its first unit
+    long long base;
+};
+
+// Where unit x of the line lies: the CTA sums every sequence's units, a run
+// of sequences per thread.  x(total) gives the unit wanted once the total is
+// known; at or past the end: seq = n_seqs.
+template <class F>
+__device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x_of) {
+    __shared__ long long s_sum[32];
+    __shared__ long long s_base;
+    __shared__ int s_seq;
+    const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.n_seqs + nt - 1) / nt;
+    const int a = min(p.n_seqs, (int)threadIdx.x * per), b = min(p.n_seqs, a + per);
+    long long mine = 0;
+    for (int s = a; s < b; ++s) mine += head_units(p, pl, seq_rows(p, s)) * p.Hk;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    if (threadIdx.x == 0) { s_seq = p.n_seqs; s_base = 0; }
+    __syncthreads();
+    Line l;
+    l.total = 0;
+    long long before = inc - mine;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        l.total += s_sum[w];
+    }
+    l.chunk = max(1ll, (l.total + n_ctas - 1) / n_ctas);
+    const long long x = x_of(l);
+    if (x >= before && x < before + mine) {
+        for (int s = a; s < b; ++s) {
+            const long long u = head_units(p, pl, seq_rows(p, s)) * p.Hk;
+            if (x < before + u) {
+                s_seq = s;
+                s_base = before;
+                break;
+            }
+            before += u;
+        }
+    }
+    __syncthreads();
+    l.seq = s_seq;
+    l.base = s_base;
+    return l;
+}
+
+// One item of the line, and how to go on to the next.
+struct Item {
+    int s, head, rt;
+    SeqRows rows;
+    Tile tile;
+    long long begin;          // first unit
+
+    __device__ void load(const AttendParams& p, const Plan& pl) { tile = tile_of(p, pl, rows, rt); }
+    // The item that holds unit x >= base of sequence seq.
+    __device__ bool seek(const AttendParams& p, const Plan& pl, int seq, long long base, long long x) {
+        s = seq;
+        if (s >= p.n_seqs) return false;
+        rows = seq_rows(p, s);
+        const long long per_head = head_units(p, pl, rows);
+        head = (int)((x - base) / per_head);
+        begin = base + head * per_head;
+        rt = 0;
+        load(p, pl);
+        while (x >= begin + tile.units) {
+            begin += tile.units;
+            ++rt;
+            load(p, pl);
+        }
+        return true;
+    }
+    __device__ bool next(const AttendParams& p, const Plan& pl) {
+        begin += tile.units;
+        if (++rt >= n_row_tiles(p, pl, rows)) {
+            rt = 0;
+            if (++head >= p.Hk) {
+                head = 0;
+                do {
+                    if (++s >= p.n_seqs) return false;
+                    rows = seq_rows(p, s);
+                } while (n_row_tiles(p, pl, rows) == 0);
+            }
+        }
+        load(p, pl);
+        return true;
+    }
+};
+
+// Floats of one part of a cut item: rows * D sums, then m and l per row.
+__host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+// ---------------------------------------------------------------------------
+// arithmetic
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four codes of a word as fp16: lo = bytes 0, 1, hi = bytes 2, 3.  int8: the
+// byte plus 128 under the exponent of 1024 is 1152 + code, minus 1152.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (FMT == LMOE_KV_INT8) {
+        lo = hsub2(prmt(w, 0x64646464u, 0x4140), 0x64806480u);
+        hi = hsub2(prmt(w, 0x64646464u, 0x4342), 0x64806480u);
+    } else {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t biased(uint32_t w) { return FMT == LMOE_KV_INT8 ? w ^ 0x80808080u : w; }
+
+// ---------------------------------------------------------------------------
+// few query rows
+// ---------------------------------------------------------------------------
+
+// D, code format, NR tiles of 8 query rows, NS warps that share a step (each
+// holding D / NS of the output columns, which bounds the accumulators to 128
+// registers).
+template <int D, int FMT, int NR, int NS>
+struct Few {
+    static constexpr int kRows = 8 * NR;
+    static constexpr int kGroups = kWarps / NS;
+    static constexpr int kSteps = D / 16;              // K steps of the score product
+    static constexpr int kKw = D / 16;                 // words of a key row per lane (D / 4 bytes)
+    static constexpr int kVw = D / 32 / NS;            // words of a value row per lane
+    static constexpr int kTiles = 2 * kVw;             // M tiles of the output product per warp
+    static constexpr int kOut = kTiles * 4 * NR;       // accumulators
+    static constexpr bool kQInRegs = kSteps * 2 * NR <= 32;
+    static constexpr size_t kQBytes = (size_t)kSteps * NR * 32 * 8;
+    static constexpr size_t kJoinBytes = (size_t)(kGroups / 2) * NS * kOut * 32 * 4;
+    static constexpr size_t kSmem = kQBytes + kJoinBytes;
+    static constexpr int kCtasPerSm = kOut <= 32 ? 2 : 1;   // 128 or 255 registers a thread
+};
+
+template <int D, int FMT, int NR, int NS>
+__global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
+    k_attend_few(AttendParams p, Plan pl) {
+    using C = Few<D, FMT, NR, NS>;
+    extern __shared__ __align__(16) char smem[];
+    uint2* qf = reinterpret_cast<uint2*>(smem);                       // query fragments [step][NR][lane]
+    float* jbuf = reinterpret_cast<float*>(smem + C::kQBytes);
+    __shared__ float s_qscale[kMaxRows];
+    __shared__ int s_pos[kMaxRows];
+    __shared__ float s_m[kWarps][kMaxRows], s_l[kWarps][kMaxRows];
+
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int grp = warp / NS, hs = warp % NS;
+    const Line line = find_unit(p, pl, gridDim.x, [&](const Line& l) { return l.chunk * blockIdx.x; });
+    long long x = line.chunk * blockIdx.x;
+    const long long x_end = min(line.total, x + line.chunk);
+    if (x >= x_end) return;
+    Item it;
+    if (!it.seek(p, pl, line.seq, line.base, x)) return;
+    const int page_mask = (1 << p.page_log2) - 1;
+
+    for (;;) {
+        const int u0 = (int)(x - it.begin);
+        const int u1 = (int)min((long long)it.tile.units, x_end - it.begin);
+        const int r0 = it.rt * C::kRows, n_rows = min(C::kRows, it.rows.n * p.G - r0);
+        const int first = it.rows.kv - it.rows.n;
+
+        // ---- queries: rows scaled by a power of two into fp16, as fragments
+        __syncthreads();
+        for (int r = warp; r < C::kRows; r += kWarps) {
+            float v[D / 32];
+            float a = 0.f;
+            const int row = r0 + r;
+            if (r < n_rows) {
+                const uint16_t* src = p.q + (size_t)(it.rows.q0 + row / p.G) * p.q_stride +
+                                      (size_t)(it.head * p.G + row % p.G) * D + lane * (D / 32);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const float2 f = bf16x2_to_f32x2(__ldg(reinterpret_cast<const uint32_t*>(src) + i));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
+            }
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                a = fmaxf(a, fabsf(v[i]));
+                bad |= !(fabsf(v[i]) <= 3.4e38f);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            bad = __any_sync(0xffffffffu, bad);
+            // 2^e with a 2^-e in [1, 2); the exponent is kept where both
+            // powers are normal
+            int e = (int)(__float_as_uint(a) >> 23) - 127;
+            e = min(max(e, -100), 126);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+            // element d of a row: step (d / 64) * 4 + (d / 4) % 4 and lane t = (d / 16) % 4
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int d = lane * (D / 32) + i;
+                const int step = (d >> 6) * 4 + ((d >> 2) & 3), tt = (d >> 4) & 3;
+                __half* f = reinterpret_cast<__half*>(qf + ((size_t)step * NR + (r >> 3)) * 32 + (r & 7) * 4 + tt);
+                f[d & 3] = __float2half_rn(bad ? 0.f : v[i] * down);
+            }
+            if (lane == 0) {
+                s_qscale[r] = bad ? __int_as_float(0x7fffffff) : up * p.scale_log2;
+                s_pos[r] = first + row / p.G;
+            }
+        }
+        __syncthreads();
+
+        float qscale[NR][2];
+        uint2 q_reg[C::kQInRegs ? C::kSteps : 1][NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            qscale[r][0] = s_qscale[8 * r + 2 * t];
+            qscale[r][1] = s_qscale[8 * r + 2 * t + 1];
+            if (C::kQInRegs) {
+#pragma unroll
+                for (int k = 0; k < C::kSteps; ++k) q_reg[k][r] = qf[((size_t)k * NR + r) * 32 + lane];
+            }
+        }
+
+        float o[C::kTiles][NR][4];
+        float m[NR][2], l[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+            for (int j = 0; j < C::kTiles; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[j][r][i] = 0.f;
+            m[r][0] = m[r][1] = -INFINITY;
+            l[r][0] = l[r][1] = 0.f;
+        }
+
+        // ---- the piece's 16-token steps, this warp's in turn
+        const int st_end = min(it.tile.step1, it.tile.step0 + u1 * C::kGroups);
+        int st = it.tile.step0 + u0 * C::kGroups + grp;
+        const int32_t* table = p.table + (size_t)it.s * p.table_stride;
+        // rows all of whose tokens every query row sees need no mask
+        const int pos_lo = p.causal ? first + r0 / p.G : it.rows.kv - 1;
+        const int pos_hi = first + (r0 + n_rows - 1) / p.G;
+        const int win_lo = p.window ? pos_hi - p.window : -1;
+
+        uint32_t kw[2][C::kKw], vw[4][C::kVw];
+        float ks[2], vs[2];
+        bool ok = false;            // the step's page exists
+        size_t row = 0;
+        auto locate = [&](int step, bool& good) -> size_t {
+            const int tok = step << 4;
+            const int page = __ldg(table + (tok >> p.page_log2));
+            good = page >= 0 && page < p.n_pages;
+            if (!good) set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+            return page_row(p, good ? page : 0, it.head) + (tok & page_mask);
+        };
+        auto load_k = [&](size_t base) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* src = p.k + (base + g + 8 * h) * D + t * 16;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 v = ldg_stream(reinterpret_cast<const uint4*>(src + i * 64));
+                    kw[h][4 * i] = v.x;
+                    kw[h][4 * i + 1] = v.y;
+                    kw[h][4 * i + 2] = v.z;
+                    kw[h][4 * i + 3] = v.w;
+                }
+                ks[h] = __ldg(p.ks + base + g + 8 * h);
+                vs[h] = __ldg(p.vs + base + g + 8 * h);
+            }
+        };
+        auto load_v = [&](size_t base) {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint8_t* src = p.v + (base + 2 * t + (h & 1) + 8 * (h >> 1)) * D;
+                if (D == 64) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + g * 8));
+                    vw[h][0] = v.x;
+                    vw[h][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::kVw / 4; ++i) {
+                        const uint4 v = ldg_stream(reinterpret_cast<const uint4*>(src + ((hs + i) * 8 + g) * 16));
+                        vw[h][4 * i] = v.x;
+                        vw[h][4 * i + 1] = v.y;
+                        vw[h][4 * i + 2] = v.z;
+                        vw[h][4 * i + 3] = v.w;
+                    }
+                }
+            }
+        };
+        size_t row_next = 0;
+        bool ok_next = false;
+        if (st < st_end) {
+            row = locate(st, ok);
+            load_k(row);
+            load_v(row);
+            if (st + C::kGroups < st_end) row_next = locate(st + C::kGroups, ok_next);
+        }
+        for (; st < st_end; st += C::kGroups) {
+            const bool more = st + C::kGroups < st_end;
+            // scores, tokens x rows
+            float s[NR][4];
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < C::kSteps; ++k) {
+                uint32_t a[4];
+                codes_to_f16<FMT>(biased<FMT>(kw[0][k]), a[0], a[2]);
+                codes_to_f16<FMT>(biased<FMT>(kw[1][k]), a[1], a[3]);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const uint2 b = C::kQInRegs ? q_reg[C::kQInRegs ? k : 0][r] : qf[((size_t)k * NR + r) * 32 + lane];
+                    mma_f16(s[r], a, b.x, b.y);
+                }
+            }
+            const float k0 = ks[0], k1 = ks[1];
+            // scales that are no positive numbers make a score NaN (a row
+            // stored as NaN) or belong to places that are masked below
+            const bool f0 = vs[0] > 0.f && vs[0] < INFINITY, f1 = vs[1] > 0.f && vs[1] < INFINITY;
+            const float lv0 = f0 ? __log2f(vs[0]) : __int_as_float(0x7fffffff);
+            const float lv1 = f1 ? __log2f(vs[1]) : __int_as_float(0x7fffffff);
+            const float iv0 = f0 ? __frcp_rn(vs[0]) : 1.f, iv1 = f1 ? __frcp_rn(vs[1]) : 1.f;
+            const int tok = st << 4;
+            const bool whole = ok && tok + 15 <= min(pos_lo, it.rows.kv - 1) && tok > win_lo;
+            const bool ok_now = ok;
+            if (more) {
+                load_k(row_next);
+                ok = ok_next;
+            }
+            float top = -INFINITY;
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                s[r][0] = fmaf(s[r][0] * k0, qscale[r][0], lv0);
+                s[r][1] = fmaf(s[r][1] * k0, qscale[r][1], lv0);
+                s[r][2] = fmaf(s[r][2] * k1, qscale[r][0], lv1);
+                s[r][3] = fmaf(s[r][3] * k1, qscale[r][1], lv1);
+            }
+            if (!whole) {
+                const int t0 = tok + g, t1 = t0 + 8;
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tk = i < 2 ? t0 : t1, pos = s_pos[8 * r + 2 * t + (i & 1)];
+                        bool seen = ok_now && tk < it.rows.kv;
+                        if (p.causal) seen = seen && tk <= pos && (!p.window || tk > pos - p.window);
+                        if (!seen) s[r][i] = -INFINITY;
+                    }
+                // codes behind the last token may be anything, a NaN code too
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    if (!ok_now || tok + 2 * t + (h & 1) + 8 * (h >> 1) >= it.rows.kv)
+#pragma unroll
+                        for (int i = 0; i < C::kVw; ++i) vw[h][i] = 0u;
+            }
+            // the running maximum is raised only when a score passes it by 8:
+            // p stays below 2^8, far inside fp16, and most steps skip the
+            // exchange between lanes and the rescaling
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top = fmaxf(s[r][i], s[r][i + 2]);
+                    grow |= top > m[r][i] + 8.f;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float n = fmaxf(s[r][i], s[r][i + 2]);
+                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
+                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
+                        n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16));
+                        n = fmaxf(n, m[r][i]);
+                        const float f = m[r][i] == n ? 1.f : ex2(m[r][i] - n);
+                        m[r][i] = n;
+                        l[r][i] *= f;
+#pragma unroll
+                        for (int j = 0; j < C::kTiles; ++j) {
+                            o[j][r][i] *= f;
+                            o[j][r][i + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pb[NR][2];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float m0 = m[r][0] == -INFINITY ? 0.f : m[r][0], m1 = m[r][1] == -INFINITY ? 0.f : m[r][1];
+                const float p0 = ex2(s[r][0] - m0), p1 = ex2(s[r][1] - m1), p2 = ex2(s[r][2] - m0), p3 = ex2(s[r][3] - m1);
+                l[r][0] = fmaf(p0, iv0, fmaf(p2, iv1, l[r][0]));
+                l[r][1] = fmaf(p1, iv0, fmaf(p3, iv1, l[r][1]));
+                const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+                pb[r][0] = movmatrix(*reinterpret_cast<const uint32_t*>(&h0));
+                pb[r][1] = movmatrix(*reinterpret_cast<const uint32_t*>(&h1));
+            }
+            // output, columns x rows
+#pragma unroll
+            for (int w = 0; w < C::kVw; ++w) {
+                const uint32_t v0 = biased<FMT>(vw[0][w]), v1 = biased<FMT>(vw[1][w]), v2 = biased<FMT>(vw[2][w]),
+                               v3 = biased<FMT>(vw[3][w]);
+                uint32_t a[2][4];
+                codes_to_f16<FMT>(prmt(v0, v1, 0x5140), a[0][0], a[0][1]);
+                codes_to_f16<FMT>(prmt(v2, v3, 0x5140), a[0][2], a[0][3]);
+                codes_to_f16<FMT>(prmt(v0, v1, 0x7362), a[1][0], a[1][1]);
+                codes_to_f16<FMT>(prmt(v2, v3, 0x7362), a[1][2], a[1][3]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma_f16(o[2 * w + j][r], a[j], pb[r][0], pb[r][1]);
+            }
+            if (more) {
+                load_v(row_next);
+                if (st + 2 * C::kGroups < st_end) row_next = locate(st + 2 * C::kGroups, ok_next);
+            }
+        }
+
+        // ---- join the warps
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[r][i] += __shfl_xor_sync(0xffffffffu, l[r][i], d);
+                if (g == 0 && hs == 0) {
+                    s_m[grp][8 * r + 2 * t + i] = m[r][i];
+                    s_l[grp][8 * r + 2 * t + i] = l[r][i];
+                }
+            }
+        __syncthreads();
+        float ltot[NR][2], mtot[NR][2];
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rr = 8 * r + 2 * t + i;
+                float n = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < C::kGroups; ++w) n = fmaxf(n, s_m[w][rr]);
+                const float nn = n == -INFINITY ? 0.f : n;
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < C::kGroups; ++w) sum += s_l[w][rr] * ex2(s_m[w][rr] - nn);
+                mtot[r][i] = n;
+                ltot[r][i] = sum;
+                const float f = ex2(m[r][i] - nn);
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j) {
+                    o[j][r][i] *= f;
+                    o[j][r][i + 2] *= f;
+                }
+            }
+#pragma unroll
+        for (int h = C::kGroups / 2; h > 0; h >>= 1) {
+            if (grp >= h && grp < 2 * h) {
+                float* b = jbuf + ((size_t)((grp - h) * NS + hs) * C::kOut) * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) b[((j * NR + r) * 4 + i) * 32] = o[j][r][i];
+            }
+            __syncthreads();
+            if (grp < h) {
+                const float* b = jbuf + ((size_t)(grp * NS + hs) * C::kOut) * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < C::kTiles; ++j)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][r][i] += b[((j * NR + r) * 4 + i) * 32];
+            }
+            __syncthreads();
+        }
+        if (grp == 0) {
+            const bool cut = u0 > 0 || u1 < it.tile.units;
+            // lane (g, t): rows 2t, 2t + 1 of each 8, columns per word w, tile
+            // pair j and half: the bytes it read of a value row
+            float* part = p.part + ((size_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = 8 * r + 2 * t + i;
+                    if (rr >= n_rows) continue;
+                    const float inv = cut ? 1.f : ltot[r][i] == 0.f ? 0.f : 1.f / ltot[r][i];
+                    const size_t orow = (size_t)(it.rows.q0 + (r0 + rr) / p.G) * p.Hq + it.head * p.G + (r0 + rr) % p.G;
+#pragma unroll
+                    for (int w = 0; w < C::kVw; ++w) {
+                        const int d = D == 64 ? g * 8 + 4 * w : ((hs + (w >> 2)) * 8 + g) * 16 + 4 * (w & 3);
+                        const float y[4] = {o[2 * w][r][i] * inv, o[2 * w][r][i + 2] * inv, o[2 * w + 1][r][i] * inv,
+                                            o[2 * w + 1][r][i + 2] * inv};
+                        if (cut) {
+                            *reinterpret_cast<float4*>(part + (size_t)rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+                        } else {
+                            const uint2 b = make_uint2(
+                                (uint32_t)f32_to_bf16_bits(y[0]) | (uint32_t)f32_to_bf16_bits(y[1]) << 16,
+                                (uint32_t)f32_to_bf16_bits(y[2]) | (uint32_t)f32_to_bf16_bits(y[3]) << 16);
+                            *reinterpret_cast<uint2*>(p.out + orow * D + d) = b;
+                        }
+                    }
+                    if (g == 0 && hs == 0) {
+                        if (cut) {
+                            part[(size_t)C::kRows * D + rr] = mtot[r][i];
+                            part[(size_t)C::kRows * (D + 1) + rr] = ltot[r][i];
+                        } else if (p.lse) {
+                            p.lse[orow] = ltot[r][i] == 0.f ? -INFINITY : (mtot[r][i] + log2f(ltot[r][i])) * 0.6931471805599453f;
+                        }
+                    }
+                }
+        }
+        x = it.begin + u1;
+        if (x >= x_end || !it.next(p, pl)) break;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// items cut between CTAs
+// ---------------------------------------------------------------------------
+
+// CTA (b, r): the item cut at the start of CTA b + 1's piece, if that is the
+// item's first cut; row r of it.  Warp w adds parts w, w + 4, ... and the four
+// sums meet in shared memory.
+constexpr int kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, Plan pl, int n_ctas) {
+    __shared__ float s_o[4][D];
+    __shared__ float s_w[4], s_max[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1, rr = blockIdx.y;
+    const Line line = find_unit(p, pl, n_ctas, [&](const Line& l) { return l.chunk * c; });
+    grid_dep_wait();
+    const long long x = line.chunk * c;
+    if (x >= line.total) return;
+    Item it;
+    if (!it.seek(p, pl, line.seq, line.base, x)) return;
+    const int r0 = it.rt * pl.rows;
+    if (it.begin == x || it.begin < x - line.chunk || rr >= min(pl.rows, it.rows.n * p.G - r0)) return;
+    const int c1 = (int)((it.begin + it.tile.units - 1) / line.chunk);   // last CTA with a part
+    const size_t pf = part_floats(pl.rows, D);
+    auto part = [&](int k) { return p.part + ((size_t)k * 2 + (k == c - 1 ? 1 : 0)) * pf; };
+    float m = -INFINITY;
+    for (int k = c - 1 + threadIdx.x; k <= c1; k += kJoinThreads) m = fmaxf(m, part(k)[(size_t)pl.rows * D + rr]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const float mm = m == -INFINITY ? 0.f : m;
+    constexpr int V = D / 32;
+    float o[V], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    for (int k = c - 1 + warp; k <= c1; k += 4) {
+        const float* q = part(k);
+        const float f = ex2(q[(size_t)pl.rows * D + rr] - mm);
+        l = fmaf(f, q[(size_t)pl.rows * (D + 1) + rr], l);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(f, q[(size_t)rr * D + lane + 32 * i], o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
+    if (lane == 0) s_w[warp] = l;
+    __syncthreads();
+    l = s_w[0] + s_w[1] + s_w[2] + s_w[3];
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t orow = (size_t)(it.rows.q0 + (r0 + rr) / p.G) * p.Hq + it.head * p.G + (r0 + rr) % p.G;
+    for (int d = threadIdx.x; d < D; d += kJoinThreads)
+        p.out[orow * D + d] = f32_to_bf16_bits((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
+    if (threadIdx.x == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D>
+cudaError_t launch_join(const AttendParams& p, const Plan& pl, int n_ctas, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n_ctas - 1, pl.rows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attend_join<D>, p, pl, n_ctas);
+}
+
+template <int D, int FMT, int NR, int NS>
+cudaError_t launch_few(const AttendParams& p, cudaStream_t st) {
+    using C = Few<D, FMT, NR, NS>;
+    const Plan pl{C::kRows, C::kGroups};
+    constexpr int kCtas = kSms * C::kCtasPerSm;
+    cudaError_t e = allow_smem<k_attend_few<D, FMT, NR, NS>>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    k_attend_few<D, FMT, NR, NS><<<kCtas, kThreads, C::kSmem, st>>>(p, pl);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_join<D>(p, pl, kCtas, st);
+}
+
+template <int D, int FMT>
+cudaError_t launch_rows(const AttendParams& p, cudaStream_t st) {
+    const long long rows = (long long)p.max_new * p.G;
+    if (rows <= 8) return launch_few<D, FMT, 1, 1>(p, st);
+    if (rows <= 16) return launch_few<D, FMT, 2, 1>(p, st);
+    return launch_few<D, FMT, 4, D == 256 ? 2 : 1>(p, st);
+}
+
+}  // namespace
+
+size_t attend_part_bytes(int D) { return kMaxCtas * 2 * part_floats(kMaxRows, D) * 4; }
+
+cudaError_t run_attend(const AttendParams& p, cudaStream_t st) {
+    const bool i8 = p.fmt == LMOE_KV_INT8;
+    if (p.D == 64) return i8 ? launch_rows<64, LMOE_KV_INT8>(p, st) : launch_rows<64, LMOE_KV_E4M3>(p, st);
+    if (p.D == 128) return i8 ? launch_rows<128, LMOE_KV_INT8>(p, st) : launch_rows<128, LMOE_KV_E4M3>(p, st);
+    return i8 ? launch_rows<256, LMOE_KV_INT8>(p, st) : launch_rows<256, LMOE_KV_E4M3>(p, st);
+}
+
+}  // namespace lmoe
