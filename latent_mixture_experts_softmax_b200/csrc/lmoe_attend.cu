@@ -26,7 +26,7 @@
 // join their results through shared memory.  An item cut between CTAs leaves
 // its parts in the workspace for k_attend_join, which adds them in order.
 
-#include "lmoe_mixers.cuh"
+#include "lmoe_attend.cuh"
 #include "lmoe_sm100.cuh"
 
 namespace lmoe {
@@ -34,161 +34,15 @@ namespace lmoe {
 namespace {
 
 using namespace sm100;
+using namespace attend;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxRows = 32;        // query rows of one item
-constexpr int kMaxCtas = 2 * kSms;
-
-// ---------------------------------------------------------------------------
-// the line of work units
-// ---------------------------------------------------------------------------
-
-struct Plan {
-    int rows;          // query rows of a row tile
-    int groups;        // 16-token steps of a unit
-};
-
-struct Tile {
-    int step0, step1;  // 16-token steps the row tile reads
-    int units;         // at least one, so that empty tiles are written too
-};
-
-__device__ __forceinline__ Tile tile_of(const AttendParams& p, const Plan& pl, const SeqRows& s, int rt) {
-    const int r0 = rt * pl.rows, r1 = min(r0 + pl.rows, s.n * p.G);
-    const int first = s.kv - s.n;
-    int lo = 0, hi = s.kv;
-    if (p.causal) {
-        hi = min(hi, first + (r1 - 1) / p.G + 1);
-        if (p.window) lo = max(0, first + r0 / p.G - p.window + 1);
-    }
-    hi = max(hi, lo);
-    Tile t;
-    t.step0 = lo >> 4;
-    t.step1 = max(t.step0, hi > lo ? (hi + 15) >> 4 : t.step0);
-    t.units = max(1, (t.step1 - t.step0 + pl.groups - 1) / pl.groups);
-    return t;
-}
-
-__device__ __forceinline__ int n_row_tiles(const AttendParams& p, const Plan& pl, const SeqRows& s) {
-    return s.n <= 0 ? 0 : (int)(((long long)s.n * p.G + pl.rows - 1) / pl.rows);
-}
-
-// Units of one head of a sequence.
-__device__ __forceinline__ long long head_units(const AttendParams& p, const Plan& pl, const SeqRows& s) {
-    long long u = 0;
-    for (int rt = 0, n = n_row_tiles(p, pl, s); rt < n; ++rt) u += tile_of(p, pl, s, rt).units;
-    return u;
-}
-
-struct Line {
-    long long total, chunk;   // units, and units per CTA
-    int seq;                  // the sequence holding unit x, and its first unit
-    long long base;
-};
-
-// Where unit x of the line lies: the CTA sums every sequence's units, a run
-// of sequences per thread.  x(total) gives the unit wanted once the total is
-// known; at or past the end: seq = n_seqs.
-template <class F>
-__device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x_of) {
-    __shared__ long long s_sum[32];
-    __shared__ long long s_base;
-    __shared__ int s_seq;
-    const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (p.n_seqs + nt - 1) / nt;
-    const int a = min(p.n_seqs, (int)threadIdx.x * per), b = min(p.n_seqs, a + per);
-    long long mine = 0;
-    for (int s = a; s < b; ++s) mine += head_units(p, pl, seq_rows(p, s)) * p.Hk;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_sum[warp] = inc;
-    if (threadIdx.x == 0) { s_seq = p.n_seqs; s_base = 0; }
-    __syncthreads();
-    Line l;
-    l.total = 0;
-    long long before = inc - mine;
-    for (int w = 0; w < nt / 32; ++w) {
-        if (w < warp) before += s_sum[w];
-        l.total += s_sum[w];
-    }
-    l.chunk = max(1ll, (l.total + n_ctas - 1) / n_ctas);
-    const long long x = x_of(l);
-    if (x >= before && x < before + mine) {
-        for (int s = a; s < b; ++s) {
-            const long long u = head_units(p, pl, seq_rows(p, s)) * p.Hk;
-            if (x < before + u) {
-                s_seq = s;
-                s_base = before;
-                break;
-            }
-            before += u;
-        }
-    }
-    __syncthreads();
-    l.seq = s_seq;
-    l.base = s_base;
-    return l;
-}
-
-// One item of the line, and how to go on to the next.
-struct Item {
-    int s, head, rt;
-    SeqRows rows;
-    Tile tile;
-    long long begin;          // first unit
-
-    __device__ void load(const AttendParams& p, const Plan& pl) { tile = tile_of(p, pl, rows, rt); }
-    // The item that holds unit x >= base of sequence seq.
-    __device__ bool seek(const AttendParams& p, const Plan& pl, int seq, long long base, long long x) {
-        s = seq;
-        if (s >= p.n_seqs) return false;
-        rows = seq_rows(p, s);
-        const long long per_head = head_units(p, pl, rows);
-        head = (int)((x - base) / per_head);
-        begin = base + head * per_head;
-        rt = 0;
-        load(p, pl);
-        while (x >= begin + tile.units) {
-            begin += tile.units;
-            ++rt;
-            load(p, pl);
-        }
-        return true;
-    }
-    __device__ bool next(const AttendParams& p, const Plan& pl) {
-        begin += tile.units;
-        if (++rt >= n_row_tiles(p, pl, rows)) {
-            rt = 0;
-            if (++head >= p.Hk) {
-                head = 0;
-                do {
-                    if (++s >= p.n_seqs) return false;
-                    rows = seq_rows(p, s);
-                } while (n_row_tiles(p, pl, rows) == 0);
-            }
-        }
-        load(p, pl);
-        return true;
-    }
-};
-
-// Floats of one part of a cut item: rows * D sums, then m and l per row.
-__host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+constexpr int kMaxRows = kFewRows;
 
 // ---------------------------------------------------------------------------
 // arithmetic
 // ---------------------------------------------------------------------------
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -203,31 +57,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
-
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Four codes of a word as fp16: lo = bytes 0, 1, hi = bytes 2, 3.  int8: the
-// byte plus 128 under the exponent of 1024 is 1152 + code, minus 1152.
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if (FMT == LMOE_KV_INT8) {
-        lo = hsub2(prmt(w, 0x64646464u, 0x4140), 0x64806480u);
-        hi = hsub2(prmt(w, 0x64646464u, 0x4342), 0x64806480u);
-    } else {
-        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    }
-}
-
-template <int FMT>
-__device__ __forceinline__ uint32_t biased(uint32_t w) { return FMT == LMOE_KV_INT8 ? w ^ 0x80808080u : w; }
 
 // ---------------------------------------------------------------------------
 // few query rows
@@ -267,11 +96,15 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int grp = warp / NS, hs = warp % NS;
     const Line line = find_unit(p, pl, gridDim.x, [&](const Line& l) { return l.chunk * blockIdx.x; });
-    long long x = line.chunk * blockIdx.x;
+    const long long x_begin = line.chunk * blockIdx.x;
+    long long x = x_begin;
     const long long x_end = min(line.total, x + line.chunk);
-    if (x >= x_end) return;
+    if (x >= x_end) {
+        if (threadIdx.x == 0) p.cuts[blockIdx.x].x = -1;
+        return;
+    }
     Item it;
-    if (!it.seek(p, pl, line.seq, line.base, x)) return;
+    it.seek(p, pl, line.seq, line.base, x);
     const int page_mask = (1 << p.page_log2) - 1;
 
     for (;;) {
@@ -636,69 +469,85 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
         x = it.begin + u1;
         if (x >= x_end || !it.next(p, pl)) break;
     }
+    if (threadIdx.x == 0) {
+        const Cut c = it.begin >= x_begin ? cut_of(line, it, x_end) : Cut{-1, 0, 0, 0};
+        p.cuts[blockIdx.x] = make_int4(c.s, c.head, c.rt, c.last);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // items cut between CTAs
 // ---------------------------------------------------------------------------
 
-// CTA (b, r): the item cut at the start of CTA b + 1's piece, if that is the
-// item's first cut; row r of it.  Warp w adds parts w, w + 4, ... and the four
-// sums meet in shared memory.
 constexpr int kJoinThreads = 128;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, Plan pl, int n_ctas) {
-    __shared__ float s_o[4][D];
-    __shared__ float s_w[4], s_max[4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x + 1, rr = blockIdx.y;
-    const Line line = find_unit(p, pl, n_ctas, [&](const Line& l) { return l.chunk * c; });
-    grid_dep_wait();
-    const long long x = line.chunk * c;
-    if (x >= line.total) return;
-    Item it;
-    if (!it.seek(p, pl, line.seq, line.base, x)) return;
-    const int r0 = it.rt * pl.rows;
-    if (it.begin == x || it.begin < x - line.chunk || rr >= min(pl.rows, it.rows.n * p.G - r0)) return;
-    const int c1 = (int)((it.begin + it.tile.units - 1) / line.chunk);   // last CTA with a part
-    const size_t pf = part_floats(pl.rows, D);
-    auto part = [&](int k) { return p.part + ((size_t)k * 2 + (k == c - 1 ? 1 : 0)) * pf; };
-    float m = -INFINITY;
-    for (int k = c - 1 + threadIdx.x; k <= c1; k += kJoinThreads) m = fmaxf(m, part(k)[(size_t)pl.rows * D + rr]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_max[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    const float mm = m == -INFINITY ? 0.f : m;
+// Block (c, b): rows of the item that CTA c began and others went on with.
+// FEW: one row a block, whose four warps take parts in turn (an item of few
+// rows may be spread over all CTAs); else four rows a warp, one after the
+// other (an item of many rows has few parts).  Parts are added in a fixed
+// order.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, int rows) {
+    constexpr int kParts = FEW ? 4 : 1;         // warps that share a row's parts
     constexpr int V = D / 32;
-    float o[V], l = 0.f;
+    __shared__ float s_o[FEW ? 4 : 1][FEW ? D : 1];
+    __shared__ float s_l[4], s_m[4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    const int4 cut = p.cuts[blockIdx.x];
+    if (cut.x < 0) return;
+    const int c = blockIdx.x, last = cut.w;
+    const SeqRows sr = seq_rows(p, cut.x);
+    const int r0 = cut.z * rows, n_rows = min(rows, sr.n * p.G - r0);
+    const size_t pf = part_floats(rows, D);
+    auto part = [&](int k) { return p.part + ((size_t)k * 2 + (k == c ? 1 : 0)) * pf; };
+    for (int i = 0; i < (FEW ? 1 : 4); ++i) {
+        const int rr = FEW ? blockIdx.y : blockIdx.y * 16 + warp * 4 + i;
+        if (rr >= n_rows) return;               // a whole block (FEW), or the warp's last rows
+        const int first = FEW ? warp : 0;
+        float m = -INFINITY;
+        for (int k = c + first; k <= last; k += kParts) m = fmaxf(m, part(k)[(size_t)rows * D + rr]);
+        if (FEW) {
+            if (lane == 0) s_m[warp] = m;
+            __syncthreads();
+            m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float o[V], l = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-    for (int k = c - 1 + warp; k <= c1; k += 4) {
-        const float* q = part(k);
-        const float f = ex2(q[(size_t)pl.rows * D + rr] - mm);
-        l = fmaf(f, q[(size_t)pl.rows * (D + 1) + rr], l);
+        for (int v = 0; v < V; ++v) o[v] = 0.f;
+        for (int k = c + first; k <= last; k += kParts) {
+            const float* q = part(k);
+            const float f = ex2(q[(size_t)rows * D + rr] - mm);
+            l = fmaf(f, q[(size_t)rows * (D + 1) + rr], l);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(f, q[(size_t)rr * D + lane + 32 * i], o[i]);
+            for (int v = 0; v < V; ++v) o[v] = fmaf(f, q[(size_t)rr * D + lane + 32 * v], o[v]);
+        }
+        if (FEW) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = o[v];
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (warp) return;
+            l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                o[v] = s_o[0][lane + 32 * v] + s_o[1][lane + 32 * v] + s_o[2][lane + 32 * v] + s_o[3][lane + 32 * v];
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t orow = (size_t)(sr.q0 + (r0 + rr) / p.G) * p.Hq + cut.y * p.G + (r0 + rr) % p.G;
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.out[orow * D + lane + 32 * v] = f32_to_bf16_bits(o[v] * inv);
+        if (lane == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) s_o[warp][lane + 32 * i] = o[i];
-    if (lane == 0) s_w[warp] = l;
-    __syncthreads();
-    l = s_w[0] + s_w[1] + s_w[2] + s_w[3];
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const size_t orow = (size_t)(it.rows.q0 + (r0 + rr) / p.G) * p.Hq + it.head * p.G + (r0 + rr) % p.G;
-    for (int d = threadIdx.x; d < D; d += kJoinThreads)
-        p.out[orow * D + d] = f32_to_bf16_bits((s_o[0][d] + s_o[1][d] + s_o[2][d] + s_o[3][d]) * inv);
-    if (threadIdx.x == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D>
-cudaError_t launch_join(const AttendParams& p, const Plan& pl, int n_ctas, cudaStream_t st) {
+}  // namespace
+
+// Starts while the attention kernel drains, and waits for it on the device.
+cudaError_t attend::launch_join(const AttendParams& p, int rows, int n_ctas, bool few, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(n_ctas - 1, pl.rows);
+    cfg.gridDim = dim3(n_ctas, few ? rows : rows / 16);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute a[1];
@@ -706,20 +555,24 @@ cudaError_t launch_join(const AttendParams& p, const Plan& pl, int n_ctas, cudaS
     a[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = a;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attend_join<D>, p, pl, n_ctas);
+    if (p.D == 64) return cudaLaunchKernelEx(&cfg, few ? k_attend_join<64, true> : k_attend_join<64, false>, p, rows);
+    if (p.D == 128) return cudaLaunchKernelEx(&cfg, few ? k_attend_join<128, true> : k_attend_join<128, false>, p, rows);
+    return cudaLaunchKernelEx(&cfg, few ? k_attend_join<256, true> : k_attend_join<256, false>, p, rows);
 }
+
+namespace {
 
 template <int D, int FMT, int NR, int NS>
 cudaError_t launch_few(const AttendParams& p, cudaStream_t st) {
     using C = Few<D, FMT, NR, NS>;
-    const Plan pl{C::kRows, C::kGroups};
+    const Plan pl{C::kRows, 4, C::kGroups};
     constexpr int kCtas = kSms * C::kCtasPerSm;
     cudaError_t e = allow_smem<k_attend_few<D, FMT, NR, NS>>(C::kSmem);
     if (e != cudaSuccess) return e;
     k_attend_few<D, FMT, NR, NS><<<kCtas, kThreads, C::kSmem, st>>>(p, pl);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_join<D>(p, pl, kCtas, st);
+    return launch_join(p, C::kRows, kCtas, true, st);
 }
 
 template <int D, int FMT>
@@ -727,14 +580,20 @@ cudaError_t launch_rows(const AttendParams& p, cudaStream_t st) {
     const long long rows = (long long)p.max_new * p.G;
     if (rows <= 8) return launch_few<D, FMT, 1, 1>(p, st);
     if (rows <= 16) return launch_few<D, FMT, 2, 1>(p, st);
-    return launch_few<D, FMT, 4, D == 256 ? 2 : 1>(p, st);
+    if (rows <= 32) return launch_few<D, FMT, 4, D == 256 ? 2 : 1>(p, st);
+    return launch_many(p, st);
 }
 
 }  // namespace
 
-size_t attend_part_bytes(int D) { return kMaxCtas * 2 * part_floats(kMaxRows, D) * 4; }
+size_t attend_ws_bytes(int D) {
+    const size_t few = kMaxCtas * part_floats(kFewRows, D), many = kSms * part_floats(many_rows(D), D);
+    return kCutBytes + 2 * 4 * (few > many ? few : many);
+}
 
-cudaError_t run_attend(const AttendParams& p, cudaStream_t st) {
+cudaError_t run_attend(AttendParams p, void* ws, cudaStream_t st) {
+    p.cuts = static_cast<int4*>(ws);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes);
     const bool i8 = p.fmt == LMOE_KV_INT8;
     if (p.D == 64) return i8 ? launch_rows<64, LMOE_KV_INT8>(p, st) : launch_rows<64, LMOE_KV_E4M3>(p, st);
     if (p.D == 128) return i8 ? launch_rows<128, LMOE_KV_INT8>(p, st) : launch_rows<128, LMOE_KV_E4M3>(p, st);

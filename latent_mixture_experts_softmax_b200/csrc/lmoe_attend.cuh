@@ -1,0 +1,209 @@
+// Attention over the 8-bit paged cache: what the kernel for few query rows,
+// the kernel for many and the joining of cut items share -- the line of work
+// units, the parts of cut items and the decoding of codes.
+#pragma once
+
+#include "lmoe_mixers.cuh"
+
+namespace lmoe {
+namespace attend {
+
+constexpr int kMaxCtas = 2 * kSms;
+constexpr int kFewRows = 32;            // query rows of an item of the kernel for few rows, at most
+
+// ---------------------------------------------------------------------------
+// the line of work units
+// ---------------------------------------------------------------------------
+
+struct Plan {
+    int rows;          // query rows of a row tile
+    int step_log2;     // tokens of a step
+    int groups;        // steps of a unit
+};
+
+struct Tile {
+    int step0, step1;  // steps the row tile reads
+    int units;         // at least one, so that empty tiles are written too
+};
+
+__device__ __forceinline__ Tile tile_of(const AttendParams& p, const Plan& pl, const SeqRows& s, int rt) {
+    const int r0 = rt * pl.rows, r1 = min(r0 + pl.rows, s.n * p.G);
+    const int first = s.kv - s.n;
+    int lo = 0, hi = s.kv;
+    if (p.causal) {
+        hi = min(hi, first + (r1 - 1) / p.G + 1);
+        if (p.window) lo = max(0, first + r0 / p.G - p.window + 1);
+    }
+    hi = max(hi, lo);
+    Tile t;
+    t.step0 = lo >> pl.step_log2;
+    t.step1 = hi > lo ? ((hi - 1) >> pl.step_log2) + 1 : t.step0;
+    t.units = max(1, (t.step1 - t.step0 + pl.groups - 1) / pl.groups);
+    return t;
+}
+
+__device__ __forceinline__ int n_row_tiles(const AttendParams& p, const Plan& pl, const SeqRows& s) {
+    return s.n <= 0 ? 0 : (int)(((long long)s.n * p.G + pl.rows - 1) / pl.rows);
+}
+
+// Units of one head of a sequence.
+__device__ __forceinline__ long long head_units(const AttendParams& p, const Plan& pl, const SeqRows& s) {
+    long long u = 0;
+    for (int rt = 0, n = n_row_tiles(p, pl, s); rt < n; ++rt) u += tile_of(p, pl, s, rt).units;
+    return u;
+}
+
+struct Line {
+    long long total, chunk;   // units, and units per CTA
+    int seq;                  // the sequence holding unit x, and its first unit
+    long long base;
+};
+
+// Where unit x of the line lies: the CTA sums every sequence's units, a run
+// of sequences per thread.  x(total) gives the unit wanted once the total is
+// known; at or past the end: seq = n_seqs.
+template <class F>
+__device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x_of) {
+    __shared__ long long s_sum[32];
+    __shared__ long long s_base;
+    __shared__ int s_seq;
+    const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = (p.n_seqs + nt - 1) / nt;
+    const int a = min(p.n_seqs, (int)threadIdx.x * per), b = min(p.n_seqs, a + per);
+    long long mine = 0;
+    for (int s = a; s < b; ++s) mine += head_units(p, pl, seq_rows(p, s)) * p.Hk;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_sum[warp] = inc;
+    if (threadIdx.x == 0) { s_seq = p.n_seqs; s_base = 0; }
+    __syncthreads();
+    Line l;
+    l.total = 0;
+    long long before = inc - mine;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += s_sum[w];
+        l.total += s_sum[w];
+    }
+    l.chunk = max(1ll, (l.total + n_ctas - 1) / n_ctas);
+    const long long x = x_of(l);
+    if (x >= before && x < before + mine) {
+        for (int s = a; s < b; ++s) {
+            const long long u = head_units(p, pl, seq_rows(p, s)) * p.Hk;
+            if (x < before + u) {
+                s_seq = s;
+                s_base = before;
+                break;
+            }
+            before += u;
+        }
+    }
+    __syncthreads();
+    l.seq = s_seq;
+    l.base = s_base;
+    return l;
+}
+
+// One item of the line, and how to go on to the next.
+struct Item {
+    int s, head, rt;
+    SeqRows rows;
+    Tile tile;
+    long long begin;          // first unit
+
+    __device__ void load(const AttendParams& p, const Plan& pl) { tile = tile_of(p, pl, rows, rt); }
+    // The item that holds unit x >= base of sequence seq.
+    __device__ bool seek(const AttendParams& p, const Plan& pl, int seq, long long base, long long x) {
+        s = seq;
+        if (s >= p.n_seqs) return false;
+        rows = seq_rows(p, s);
+        const long long per_head = head_units(p, pl, rows);
+        head = (int)((x - base) / per_head);
+        begin = base + head * per_head;
+        rt = 0;
+        load(p, pl);
+        while (x >= begin + tile.units) {
+            begin += tile.units;
+            ++rt;
+            load(p, pl);
+        }
+        return true;
+    }
+    __device__ bool next(const AttendParams& p, const Plan& pl) {
+        begin += tile.units;
+        if (++rt >= n_row_tiles(p, pl, rows)) {
+            rt = 0;
+            if (++head >= p.Hk) {
+                head = 0;
+                do {
+                    if (++s >= p.n_seqs) return false;
+                    rows = seq_rows(p, s);
+                } while (n_row_tiles(p, pl, rows) == 0);
+            }
+        }
+        load(p, pl);
+        return true;
+    }
+};
+
+// Floats of one part of a cut item: rows * D sums, then m and l per row.
+__host__ __device__ constexpr size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+// A CTA whose last item goes on in the next CTAs: the item, and the last CTA
+// that has a part of it; s < 0: none.  Its own part is the CTA's second, the
+// others' parts are their first.
+struct Cut {
+    int s, head, rt, last;
+};
+
+__device__ __forceinline__ Cut cut_of(const Line& l, const Item& it, long long x_end) {
+    if (it.begin + it.tile.units <= x_end) return Cut{-1, 0, 0, 0};
+    return Cut{it.s, it.head, it.rt, (int)((it.begin + it.tile.units - 1) / l.chunk)};
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Four codes of a word as fp16: lo = bytes 0, 1, hi = bytes 2, 3.  int8: the
+// byte plus 128 under the exponent of 1024 is 1152 + code, minus 1152.
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (FMT == LMOE_KV_INT8) {
+        lo = hsub2(prmt(w, 0x64646464u, 0x4140), 0x64806480u);
+        hi = hsub2(prmt(w, 0x64646464u, 0x4342), 0x64806480u);
+    } else {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t biased(uint32_t w) { return FMT == LMOE_KV_INT8 ? w ^ 0x80808080u : w; }
+
+// Query rows of an item of the kernel for many rows: two tensor-core tiles of
+// 128, or one where the accumulators of one fill tensor memory's half.
+__host__ __device__ constexpr int many_rows(int D) { return D == 256 ? 128 : 256; }
+
+constexpr size_t kCutBytes = 8192;      // kMaxCtas records of 16 bytes
+static_assert(kMaxCtas * 16 <= kCutBytes, "cut records");
+
+cudaError_t launch_join(const AttendParams& p, int rows, int n_ctas, bool few, cudaStream_t st);
+cudaError_t launch_many(const AttendParams& p, cudaStream_t st);
+
+}  // namespace attend
+}  // namespace lmoe

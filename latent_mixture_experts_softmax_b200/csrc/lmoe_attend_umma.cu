@@ -1,0 +1,665 @@
+// Attention over the 8-bit paged cache, many query rows per key head: prompt
+// chunks.
+//
+// The mathematics is that of the kernel for few rows (lmoe_attend.cu); the
+// products run on tcgen05 (kind::f16, fp32 accumulators in tensor memory).
+// What bounds it: the tensor cores (4 D flops per row and key) and, close
+// behind, the exponentials (one per row and key, 16 a cycle and SM).
+//
+// A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
+// (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
+// 128 (64) tokens:
+//   warps 8-11   read the codes of a tile (registers, one tile ahead) and
+//                write them as fp16 operands with the 128-byte swizzle; a
+//                key row is K-major as it is stored, and the same layout
+//                read as MN-major is the value operand, so neither is
+//                transposed.  With one query tile, warps 4-7 take the keys.
+//   warp 12      one thread issues S = Q K^T and O += P V
+//   warps 0-3    softmax of query tile 0: a thread owns a row; S comes from
+//   (4-7: 1)     tensor memory, P goes back over it as the A operand.
+// With two query tiles the softmax of one runs beside the products of the
+// other; with one, two score buffers let the next S run ahead.  The row
+// maximum is raised only when a score passes it by 2^8 (p stays far inside
+// fp16), so O is rarely rescaled.
+//
+// Work is cut into equal pieces of the line of (item, key tile) units as in
+// the kernel for few rows, one piece per CTA; cut items are joined after it.
+
+#include "lmoe_attend.cuh"
+#include "lmoe_sm100.cuh"
+
+namespace lmoe {
+
+namespace {
+
+using namespace sm100;
+using namespace attend;
+
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12;
+constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
+
+template <int D>
+struct Many {
+    static constexpr int NQ = D == 256 ? 1 : 2;       // query tiles of 128 rows
+    static constexpr int TK = D == 256 ? 64 : 128;    // tokens of a key tile
+    static constexpr int kRows = NQ * 128;
+    static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
+    static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
+    static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
+    static constexpr size_t kSmem = 1024 + NQ * kQBytes + 4 * kOpBytes + 2 * kScaleBytes + 256;
+    static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 (b * TK), sums from 256 (q * D)
+};
+
+// Registers of a thread of the softmax, converting and issuing warps; the
+// sum over the four warpgroups is what the block is launched with, 4 x 128.
+template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// MN-major operand: 64 elements of N (128 bytes, swizzled) by 8 of K per
+// 1024-byte atom; atoms of the next 8 K follow, the next 64 N are lbo away.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFF) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+constexpr uint32_t kTransposeB = 1u << 16;   // instruction descriptor: B is MN-major
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pairs of fp32 in one instruction.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The CTA's piece of the line, item by item.
+struct Walk {
+    Item it;
+    long long x, x_end;
+    int u0, u1;       // units of the item in this piece
+    int t0, t1;       // its key tiles
+    int n_rows;
+
+    __device__ void open(const AttendParams& p, const Plan& pl) {
+        u0 = (int)(x - it.begin);
+        u1 = (int)min((long long)it.tile.units, x_end - it.begin);
+        t0 = it.tile.step0 + u0;
+        t1 = min(it.tile.step1, it.tile.step0 + u1);
+        n_rows = min(pl.rows, it.rows.n * p.G - it.rt * pl.rows);
+    }
+    __device__ bool next(const AttendParams& p, const Plan& pl) {
+        x = it.begin + u1;
+        if (x >= x_end || !it.next(p, pl)) return false;
+        open(p, pl);
+        return true;
+    }
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
+    using C = Many<D>;
+    constexpr int NQ = C::NQ, TK = C::TK;
+    extern __shared__ char smem_raw[];
+    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    char* sq = smem;
+    char* sk = sq + NQ * C::kQBytes;
+    char* sv = sk + 2 * C::kOpBytes;
+    float* ssc = reinterpret_cast<float*>(sv + 2 * C::kOpBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ssc) + 2 * C::kScaleBytes);
+    uint64_t* k_full = bars;         // [2] keys and scales of a stage written (4 warps)
+    uint64_t* v_full = bars + 2;     // [2]
+    uint64_t* k_empty = bars + 4;    // [2] read by the tensor core (commit)
+    uint64_t* v_empty = bars + 6;    // [2]
+    uint64_t* s_full = bars + 8;     // [2] scores of a buffer done (commit)
+    uint64_t* p_full = bars + 10;    // [2] probabilities written (4 warps)
+    uint64_t* o_done = bars + 12;    // [2] sums of a query tile updated (commit)
+    uint64_t* q_full = bars + 14;    // [2] query tile written (4 warps)
+    uint64_t* sc_free = bars + 16;   // [2] scales of a stage read (4 NQ warps)
+    uint64_t* final_bar = bars + 18;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&v_full[i], 4);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&q_full[i], 4);
+            mbar_init(&sc_free[i], 4 * NQ);
+        }
+        mbar_init(final_bar, 1);
+        *abort_flag = 0;
+        p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    grid_dep_launch();
+    tc_fence_before();
+    __syncwarp();
+    const Line line = find_unit(p, pl, gridDim.x, [&](const Line& l) { return l.chunk * blockIdx.x; });
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const long long x_begin = line.chunk * blockIdx.x;
+    Walk w;
+    w.x = x_begin;
+    w.x_end = min(line.total, x_begin + line.chunk);
+    bool more = w.x < w.x_end;
+    if (more) {
+        w.it.seek(p, pl, line.seq, line.base, w.x);
+        w.open(p, pl);
+    }
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1, abort_flag, kWaitLimit); };
+
+    if (warp < 4 * NQ) {
+        // ------------------------------------------------------ softmax
+        regs_up<NQ == 2 ? 168 : 200>();
+        const int q = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tO = tmem + lanes + C::kColO + q * D;
+        uint32_t n = 0, cnt = 0;     // key tiles of the CTA, and those of this query tile
+        bool dead = false;
+        while (more && !dead) {
+            const int r = q * 128 + row;
+            const bool live = r < w.n_rows;
+            const bool active = q * 128 < w.n_rows;      // the query tile has rows
+            const int rowid = w.it.rt * C::kRows + r;
+            const size_t orow = (size_t)(w.it.rows.q0 + rowid / p.G) * p.Hq + w.it.head * p.G + rowid % p.G;
+            const int pos = w.it.rows.kv - w.it.rows.n + rowid / p.G;
+            float m = -INFINITY, l = 0.f;
+            if (active && w.t0 < w.t1) {
+                // this row as fp16, scaled by a power of two
+                float a = 0.f, scale = 0.f;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.q + (size_t)(w.it.rows.q0 + rowid / p.G) * p.q_stride + (size_t)(w.it.head * p.G + rowid % p.G) * D);
+                char* dst = sq + q * C::kQBytes + row * 128;
+                uint32_t mb = 0;
+                if (live)
+#pragma unroll 4
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 v = __ldg(src + i);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mb = max(mb, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+                    }
+                a = bf16_bits_to_f32(mb);
+                const bool bad = mb >= 0x7f80u;
+                int e = (int)(__float_as_uint(a) >> 23) - 127;
+                e = min(max(e, -100), 126);
+                const float down = bad ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
+                scale = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23) * p.scale_log2;
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                    uint4 o = make_uint4(0, 0, 0, 0);
+                    if (live && !bad) {
+                        const uint4 v = __ldg(src + i);
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = bf16x2_to_f32x2(u[j]);
+                            const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
+                            h[j] = *reinterpret_cast<const uint32_t*>(&hh);
+                        }
+                        o = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (row & 7)) << 4)) = o;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[q]);
+                const f2 scale2 = pack2(scale, scale);
+
+                for (int t = w.t0; t < w.t1; ++t, ++n, ++cnt) {
+                    const int st = n & 1, b = NQ == 2 ? q : st;
+                    const uint32_t sph = NQ == 2 ? cnt : n >> 1;
+                    dead = !wait(&k_full[st], n >> 1) || !wait(&s_full[b], sph);
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (dead) break;
+                    tc_fence_after();
+                    __syncwarp();
+                    const uint32_t tS = tmem + lanes + b * TK;
+                    uint32_t s[TK / 32][32];
+#pragma unroll
+                    for (int c = 0; c < TK / 32; ++c) tmem_ld_32x32b_x32(tS + 32 * c, s[c]);
+                    tmem_ld_wait();
+                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
+                    const float4* lv = ks + TK / 4;
+                    const float4* iv = lv + TK / 4;
+                    const int tok0 = t * TK;
+                    // keys this row sees: columns lo .. hi - 1
+                    const int hi = p.causal ? pos + 1 - tok0 : TK;
+                    const int lo = p.window ? pos + 1 - p.window - tok0 : 0;
+                    const bool mask = __any_sync(0xffffffffu, hi < TK || lo > 0);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < TK / 4; ++c) {
+                        const float4 k4 = ks[c], b4 = lv[c];
+                        uint32_t* x = &s[c / 8][(c & 7) * 4];
+                        const f2 y0 = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y));
+                        const f2 y1 = fma2(mul2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), pack2(k4.z, k4.w)), scale2, pack2(b4.z, b4.w));
+                        float2 z0 = unpack2(y0), z1 = unpack2(y1);
+                        if (mask) {
+                            z0.x = 4 * c >= lo && 4 * c < hi ? z0.x : -INFINITY;
+                            z0.y = 4 * c + 1 >= lo && 4 * c + 1 < hi ? z0.y : -INFINITY;
+                            z1.x = 4 * c + 2 >= lo && 4 * c + 2 < hi ? z1.x : -INFINITY;
+                            z1.y = 4 * c + 3 >= lo && 4 * c + 3 < hi ? z1.y : -INFINITY;
+                        }
+                        x[0] = __float_as_uint(z0.x);
+                        x[1] = __float_as_uint(z0.y);
+                        x[2] = __float_as_uint(z1.x);
+                        x[3] = __float_as_uint(z1.y);
+                        top = fmaxf(fmaxf(top, fmaxf(z0.x, z0.y)), fmaxf(z1.x, z1.y));
+                    }
+                    if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = m == mn ? 1.f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (t > w.t0) {       // the sums of the earlier tiles are in tensor memory
+                            dead = !wait(&o_done[q], cnt - 1);
+                            dead = __any_sync(0xffffffffu, dead);
+                            if (dead) break;
+                            tc_fence_after();
+                            __syncwarp();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32(tO + 32 * c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st_32x32b_x32(tO + 32 * c, o);
+                            }
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    const f2 m2 = pack2(-mm, -mm);
+                    f2 l2 = pack2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < TK / 64; ++c) {
+                        uint32_t ph[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int col = 64 * c + 4 * i;
+                            const float4 i4 = iv[col / 4];
+                            const uint32_t* x = &s[col / 32][col & 31];
+                            const float2 y0 = unpack2(add2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), m2));
+                            const float2 y1 = unpack2(add2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), m2));
+                            const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                            l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
+                            l2 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2);
+                            const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+                            ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+                            ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        }
+                        tmem_st_32x32b_x32(tS + 32 * c, ph);
+                    }
+                    const float2 ls = unpack2(l2);
+                    l += ls.x + ls.y;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&p_full[b]);
+                        mbar_arrive(&sc_free[st]);
+                    }
+                }
+                if (dead) break;
+                dead = !wait(&o_done[q], cnt - 1);
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) break;
+                tc_fence_after();
+                __syncwarp();
+            } else {
+                for (int t = w.t0; t < w.t1; ++t, ++n) {      // a query tile without rows only lets the scales go
+                    dead = !wait(&k_full[n & 1], n >> 1);
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (dead) break;
+                    if (lane == 0) mbar_arrive(&sc_free[n & 1]);
+                }
+                if (dead) break;
+            }
+            if (active) {
+                const bool cut = w.u0 > 0 || w.u1 < w.it.tile.units;
+                const bool some = w.t0 < w.t1;
+                const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                float* part = p.part + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (some) {
+                        tmem_ld_32x32b_x32(tO + 32 * c, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
+                    if (live && cut) {
+                        float4* d = reinterpret_cast<float4*>(part + (size_t)r * D + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    } else if (live) {
+                        uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                h[j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j]) * inv) |
+                                       (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j + 1]) * inv) << 16;
+                            d[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (live && cut) {
+                    part[(size_t)C::kRows * D + r] = m;
+                    part[(size_t)C::kRows * (D + 1) + r] = l;
+                } else if (live && p.lse) {
+                    p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                }
+                tc_fence_before();      // O has been read before the next item's first P is announced
+            }
+            if (threadIdx.x == 0) {
+                const bool goes_on = w.u0 == 0 && w.u1 < w.it.tile.units;
+                const Cut c = goes_on ? cut_of(line, w.it, w.x_end) : Cut{-1, 0, 0, 0};
+                p.cuts[blockIdx.x] = make_int4(c.s, c.head, c.rt, c.last);   // the last item's stands
+            }
+            more = w.next(p, pl);
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------ converters
+        if (NQ == 2) regs_down<112>();
+        else regs_down<120>();
+        const bool do_k = NQ == 2 || warp < 8, do_v = NQ == 2 || warp >= 8;
+        const int tid = threadIdx.x & 127;
+        constexpr int CPR = D / 16;              // 16-byte pieces of a row
+        constexpr int RPP = 128 / CPR;           // rows of a pass
+        constexpr int PASSES = TK / RPP;
+        const int c16 = tid % CPR, r_first = tid / CPR;
+        const int page_mask = (1 << p.page_log2) - 1;
+        uint4 kr[PASSES], vr[PASSES];
+        float ksc = 0.f, vsc = 1.f;
+        bool sc_ok = false;
+        int pid = -1, tok0 = 0, kv = 0, head = 0;     // lane i: page of tokens 16 i .. of the tile, -1: none
+        auto locate = [&](int t) {
+            tok0 = t * TK;
+            kv = w.it.rows.kv;
+            head = w.it.head;
+            pid = -1;
+            const int tok = tok0 + 16 * lane;
+            if (lane < TK / 16 && tok < kv) {
+                pid = __ldg(p.table + (size_t)w.it.s * p.table_stride + (tok >> p.page_log2));
+                if (pid < 0 || pid >= p.n_pages) {
+                    set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+                    pid = -1;
+                }
+            }
+        };
+        auto fetch = [&](uint4 (&raw)[PASSES], const uint8_t* codes) {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r_first + i * RPP;
+                const int pg = __shfl_sync(0xffffffffu, pid, r >> 4);
+                raw[i] = make_uint4(0, 0, 0, 0);
+                if (pg >= 0 && tok0 + r < kv)
+                    raw[i] = ldg_stream(reinterpret_cast<const uint4*>(
+                        codes + (page_row(p, pg, head) + ((tok0 + r) & page_mask)) * D + c16 * 16));
+            }
+        };
+        auto fetch_scales = [&]() {
+            const int pg = __shfl_sync(0xffffffffu, pid, (tid & (TK - 1)) >> 4);
+            sc_ok = pg >= 0 && tid < TK && tok0 + tid < kv;
+            if (sc_ok) {
+                const size_t at = page_row(p, pg, head) + ((tok0 + tid) & page_mask);
+                ksc = __ldg(p.ks + at);
+                vsc = __ldg(p.vs + at);
+            }
+        };
+        auto convert = [&](const uint4 (&raw)[PASSES], char* dst) {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r_first + i * RPP;
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) codes_to_f16<FMT>(biased<FMT>(u[j]), h[2 * j], h[2 * j + 1]);
+                char* d = dst + (c16 >> 2) * (TK * 128) + r * 128;
+                // pieces of the second 64 columns write their halves in the
+                // other order: eight lanes then cover all banks
+                const int sw = (c16 >> 2) & 1, c0 = 2 * (c16 & 3);
+                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4*>(d + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? b : a;
+                *reinterpret_cast<uint4*>(d + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? a : b;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        int t = w.t0;
+        auto settle = [&]() {                    // to the next key tile there is
+            while (more && t >= w.t1) {
+                more = w.next(p, pl);
+                t = w.t0;
+            }
+        };
+        settle();
+        if (more) {
+            locate(t);
+            if (do_k) { fetch(kr, p.k); fetch_scales(); }
+            if (do_v) fetch(vr, p.v);
+        }
+        uint32_t n = 0;
+        while (more) {
+            const int st = n & 1;
+            const uint32_t ph = (n >> 1) ^ 1;
+            bool dead = false;
+            if (do_k) {
+                dead = !wait(&sc_free[st], ph) || !wait(&k_empty[st], ph);
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) break;
+                if (tid < TK) {
+                    // a place without a token weighs nothing; a scale that is
+                    // no positive number makes its token's scores NaN
+                    float* sc = ssc + st * (C::kScaleBytes / 4) + tid;
+                    const bool fine = vsc > 0.f && vsc < INFINITY;
+                    sc[0] = sc_ok ? ksc : 0.f;
+                    sc[TK] = !sc_ok ? -INFINITY : fine ? __log2f(vsc) : __int_as_float(0x7fffffff);
+                    sc[2 * TK] = sc_ok && fine ? __frcp_rn(vsc) : 1.f;
+                }
+                convert(kr, sk + st * C::kOpBytes);
+                if (lane == 0) mbar_arrive(&k_full[st]);
+            }
+            ++t;
+            settle();
+            if (more) {
+                locate(t);
+                if (do_k) { fetch(kr, p.k); fetch_scales(); }
+            }
+            if (do_v) {
+                dead = !wait(&v_empty[st], ph);
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) break;
+                convert(vr, sv + st * C::kOpBytes);
+                if (lane == 0) mbar_arrive(&v_full[st]);
+                if (more) fetch(vr, p.v);
+            }
+            ++n;
+        }
+    } else {
+        // ------------------------------------------------------ issue
+        if (NQ == 2) regs_down<64>();
+        else regs_down<72>();
+        if (warp == kMmaWarp && lane == 0) {
+            const uint32_t idesc_s = idesc_f16(128, TK, 0), idesc_o = idesc_f16(128, D, 0) | kTransposeB;
+            const uint32_t q_base = smem_u32(sq), k_base = smem_u32(sk), v_base = smem_u32(sv);
+            auto scores = [&](int q, int b, int st) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    umma_f16(tmem + b * TK, sdesc_k128(q_base + q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32),
+                             sdesc_k128(k_base + st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32), idesc_s, k > 0);
+                umma_commit(&s_full[b]);
+            };
+            auto sums = [&](int q, int b, int st, bool first) {
+#pragma unroll
+                for (int k = 0; k < TK / 16; ++k)
+                    umma_f16_ts(tmem + C::kColO + q * D, tmem + b * TK + 8 * k,
+                                sdesc_mn128(v_base + st * C::kOpBytes + k * 2048, TK * 128), idesc_o, !first || k > 0);
+                umma_commit(&o_done[q]);
+            };
+            uint32_t n = 0, cnt[2] = {0, 0}, qc[2] = {0, 0};
+            bool ok = true, issued = false;
+            while (more && ok) {
+                const int J = w.t1 - w.t0;
+                const int nq = NQ == 2 && w.n_rows > 128 ? 2 : 1;
+                if (J > 0) {
+                    for (int q = 0; q < nq && ok; ++q) ok = wait(&q_full[q], qc[q]++);
+                    if (ok) ok = wait(&k_full[n & 1], n >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issued = true;
+                    for (int q = 0; q < nq; ++q) scores(q, NQ == 2 ? q : n & 1, n & 1);
+                    umma_commit(&k_empty[n & 1]);
+                    for (int j = 0; j < J && ok; ++j, ++n) {
+                        const int st = n & 1, st1 = st ^ 1;
+                        const bool ahead = j + 1 < J;
+                        if (NQ == 1) {
+                            if (ahead) {
+                                ok = wait(&k_full[st1], (n + 1) >> 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                scores(0, st1, st1);
+                                umma_commit(&k_empty[st1]);
+                            }
+                            ok = wait(&v_full[st], n >> 1) && wait(&p_full[st], n >> 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            sums(0, st, st, j == 0);
+                        } else {
+                            ok = wait(&v_full[st], n >> 1);
+                            for (int q = 0; q < nq && ok; ++q) {
+                                ok = wait(&p_full[q], cnt[q]++);
+                                if (!ok) break;
+                                tc_fence_after();
+                                sums(q, q, st, j == 0);
+                                if (ahead) {
+                                    if (q == 0) {
+                                        ok = wait(&k_full[st1], (n + 1) >> 1);
+                                        if (!ok) break;
+                                        tc_fence_after();
+                                    }
+                                    scores(q, q, st1);
+                                }
+                            }
+                            if (!ok) break;
+                            if (ahead) umma_commit(&k_empty[st1]);
+                        }
+                        umma_commit(&v_empty[st]);
+                    }
+                }
+                if (ok) more = w.next(p, pl);
+            }
+            if (issued) {
+                // every MMA done before tensor memory is freed, even after an abort
+                umma_commit(final_bar);
+                volatile int no_abort = 0;
+                mbar_wait(final_bar, 0, &no_abort, kWaitLimit);
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag) set_status(p.ctrl, LMOE_ERR_TIMEOUT);
+}
+
+template <int D, int FMT>
+cudaError_t launch(const AttendParams& p, cudaStream_t st) {
+    using C = Many<D>;
+    static_assert(C::kRows == many_rows(D), "rows of an item");
+    const Plan pl{C::kRows, D == 256 ? 6 : 7, 1};
+    cudaError_t e = allow_smem<k_attend_many<D, FMT>>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    k_attend_many<D, FMT><<<kSms, kThreads, C::kSmem, st>>>(p, pl);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_join(p, C::kRows, kSms, false, st);
+}
+
+}  // namespace
+
+cudaError_t attend::launch_many(const AttendParams& p, cudaStream_t st) {
+    const bool i8 = p.fmt == LMOE_KV_INT8;
+    if (p.D == 64) return i8 ? launch<64, LMOE_KV_INT8>(p, st) : launch<64, LMOE_KV_E4M3>(p, st);
+    if (p.D == 128) return i8 ? launch<128, LMOE_KV_INT8>(p, st) : launch<128, LMOE_KV_E4M3>(p, st);
+    return i8 ? launch<256, LMOE_KV_INT8>(p, st) : launch<256, LMOE_KV_E4M3>(p, st);
+}
+
+}  // namespace lmoe

@@ -76,7 +76,8 @@ struct AttendParams : KvParams {
     int causal, window;
     uint16_t* out;
     float* lse;
-    float* part;           // partial results of items cut between CTAs
+    int4* cuts;            // per CTA: the item it began and others go on with
+    float* part;           // parts of items cut between CTAs
 };
 
 struct DeltaParams {
@@ -102,8 +103,8 @@ cudaError_t run_kv_append(const KvParams& p, const uint16_t* k, const uint16_t* 
                           cudaStream_t st);
 cudaError_t run_kv_read(const KvParams& p, uint16_t* k, uint16_t* v, size_t k_stride, size_t v_stride,
                         cudaStream_t st);
-size_t attend_part_bytes(int D);
-cudaError_t run_attend(const AttendParams& p, cudaStream_t st);
+size_t attend_ws_bytes(int D);
+cudaError_t run_attend(AttendParams p, void* ws, cudaStream_t st);
 size_t delta_chunk_ws_bytes(int H, int DK, int DV, int n_tokens, int n_seqs, int max_new);
 cudaError_t run_delta(const DeltaParams& p, cudaStream_t st);
 

@@ -24,7 +24,7 @@ int check_attn(const lmoe_attn_cfg* c) {
     return LMOE_OK;
 }
 
-size_t attn_ws(const lmoe_attn_cfg& c) { return kAttnCtrlBytes + attend_part_bytes(c.head_dim); }
+size_t attn_ws(const lmoe_attn_cfg& c) { return kAttnCtrlBytes + attend_ws_bytes(c.head_dim); }
 
 // Checks what every call on a cache shares and fills the parameters; *empty:
 // a valid call without anything to do.
@@ -133,8 +133,7 @@ int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe
     p.window = window;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
-    p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kAttnCtrlBytes);
-    return cuda_status(run_attend(p, static_cast<cudaStream_t>(stream)));
+    return cuda_status(run_attend(p, static_cast<char*>(ws) + kAttnCtrlBytes, static_cast<cudaStream_t>(stream)));
 }
 
 int lmoe_delta_cfg_check(const lmoe_delta_cfg* cfg) { return check_delta(cfg); }
