@@ -46,10 +46,30 @@ __device__ __forceinline__ int n_row_tiles(const AttendParams& p, const Plan& pl
     return s.n <= 0 ? 0 : (int)(((long long)s.n * p.G + pl.rows - 1) / pl.rows);
 }
 
-// Units of one head of a sequence.
+// Units of one head of a sequence, all lanes of a warp together.
 __device__ __forceinline__ long long head_units(const AttendParams& p, const Plan& pl, const SeqRows& s) {
     long long u = 0;
-    for (int rt = 0, n = n_row_tiles(p, pl, s); rt < n; ++rt) u += tile_of(p, pl, s, rt).units;
+    for (int rt = threadIdx.x & 31, n = n_row_tiles(p, pl, s); rt < n; rt += 32) u += tile_of(p, pl, s, rt).units;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    return u;
+}
+
+// The same for each lane's own sequence (s >= n_seqs: 0).
+__device__ __forceinline__ long long lane_units(const AttendParams& p, const Plan& pl, int s) {
+    SeqRows r{0, -1, 0};
+    if (s < p.n_seqs) r = seq_rows(p, s);
+    const int n = n_row_tiles(p, pl, r);
+    long long u = 0;
+    if (n <= 2)
+        for (int rt = 0; rt < n; ++rt) u += tile_of(p, pl, r, rt).units;
+    for (unsigned todo = __ballot_sync(0xffffffffu, n > 2); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        const SeqRows o{__shfl_sync(0xffffffffu, r.q0, from), __shfl_sync(0xffffffffu, r.n, from),
+                        __shfl_sync(0xffffffffu, r.kv, from)};
+        const long long v = head_units(p, pl, o);
+        if ((threadIdx.x & 31) == from) u = v;
+    }
     return u;
 }
 
@@ -69,9 +89,9 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
     __shared__ int s_seq;
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.n_seqs + nt - 1) / nt;
-    const int a = min(p.n_seqs, (int)threadIdx.x * per), b = min(p.n_seqs, a + per);
+    const int a = (int)min((long long)p.n_seqs, (long long)threadIdx.x * per), b = min(p.n_seqs, a + per);
     long long mine = 0;
-    for (int s = a; s < b; ++s) mine += head_units(p, pl, seq_rows(p, s)) * p.Hk;
+    for (int i = 0; i < per; ++i) mine += lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hk;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -90,13 +110,12 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
     }
     l.chunk = max(1ll, (l.total + n_ctas - 1) / n_ctas);
     const long long x = x_of(l);
-    if (x >= before && x < before + mine) {
-        for (int s = a; s < b; ++s) {
-            const long long u = head_units(p, pl, seq_rows(p, s)) * p.Hk;
-            if (x < before + u) {
-                s_seq = s;
+    if (__any_sync(0xffffffffu, x >= before && x < before + mine)) {
+        for (int i = 0; i < per; ++i) {
+            const long long u = lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hk;
+            if (x >= before && x < before + u) {
+                s_seq = a + i;
                 s_base = before;
-                break;
             }
             before += u;
         }
@@ -115,7 +134,8 @@ struct Item {
     long long begin;          // first unit
 
     __device__ void load(const AttendParams& p, const Plan& pl) { tile = tile_of(p, pl, rows, rt); }
-    // The item that holds unit x >= base of sequence seq.
+    // The item that holds unit x >= base of sequence seq (all lanes of a warp
+    // together).
     __device__ bool seek(const AttendParams& p, const Plan& pl, int seq, long long base, long long x) {
         s = seq;
         if (s >= p.n_seqs) return false;
@@ -123,13 +143,26 @@ struct Item {
         const long long per_head = head_units(p, pl, rows);
         head = (int)((x - base) / per_head);
         begin = base + head * per_head;
-        rt = 0;
-        load(p, pl);
-        while (x >= begin + tile.units) {
-            begin += tile.units;
-            ++rt;
-            load(p, pl);
+        const int n = n_row_tiles(p, pl, rows), lane = threadIdx.x & 31;
+        for (rt = 0;; rt += 32) {
+            const long long u = rt + lane < n ? tile_of(p, pl, rows, rt + lane).units : 0;
+            long long inc = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, x < begin + inc);
+            const int at = in ? __ffs(in) - 1 : 31;
+            if (in) {
+                begin += __shfl_sync(0xffffffffu, inc - u, at);
+                rt += at;
+                break;
+            }
+            begin += __shfl_sync(0xffffffffu, inc, 31);
+            if (rt + 32 >= n) return false;      // (x lies in the sequence, so this is not reached)
         }
+        load(p, pl);
         return true;
     }
     __device__ bool next(const AttendParams& p, const Plan& pl) {

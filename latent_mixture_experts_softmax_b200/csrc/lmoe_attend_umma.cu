@@ -9,18 +9,23 @@
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
 // 128 (64) tokens:
-//   warps 8-11   read the codes of a tile (registers, one tile ahead) and
-//                write them as fp16 operands with the 128-byte swizzle; a
-//                key row is K-major as it is stored, and the same layout
-//                read as MN-major is the value operand, so neither is
-//                transposed.  With one query tile, warps 4-7 take the keys.
-//   warp 12      one thread issues S = Q K^T and O += P V
-//   warps 0-3    softmax of query tile 0: a thread owns a row; S comes from
-//   (4-7: 1)     tensor memory, P goes back over it as the A operand.
+//   softmax      four warps per query tile: a thread owns a row; S comes from
+//                tensor memory in pieces of 32 columns, P goes back over it as
+//                the A operand.
+//   keys, values four warps each read the codes of a tile (registers, one tile
+//                ahead) and write them as fp16 operands with the 128-byte
+//                swizzle; a key row is K-major as it is stored, and the same
+//                layout read as MN-major is the value operand, so neither is
+//                transposed.
+//   issue        one thread: S = Q K^T and O += P V
 // With two query tiles the softmax of one runs beside the products of the
 // other; with one, two score buffers let the next S run ahead.  The row
 // maximum is raised only when a score passes it by 2^8 (p stays far inside
-// fp16), so O is rarely rescaled.
+// fp16), and to a whole number, so that what it rescales (O, and the P of the
+// tile's earlier pieces) changes by a power of two: the scores are gone
+// through once, and the loop stays small enough for the instruction caches
+// (a form that held a tile's scores in registers, unrolled, spent a third of
+// its time waiting for instructions).
 //
 // Work is cut into equal pieces of the line of (item, key tile) units as in
 // the kernel for few rows, one piece per CTA; cut items are joined after it.
@@ -35,8 +40,6 @@ namespace {
 using namespace sm100;
 using namespace attend;
 
-constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12;
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 
 template <int D>
@@ -44,17 +47,14 @@ struct Many {
     static constexpr int NQ = D == 256 ? 1 : 2;       // query tiles of 128 rows
     static constexpr int TK = D == 256 ? 64 : 128;    // tokens of a key tile
     static constexpr int kRows = NQ * 128;
+    static constexpr int kKeyWarp = 4 * NQ, kValueWarp = kKeyWarp + 4, kMmaWarp = kValueWarp + 4;
+    static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
     static constexpr size_t kSmem = 1024 + NQ * kQBytes + 4 * kOpBytes + 2 * kScaleBytes + 256;
     static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 (b * TK), sums from 256 (q * D)
 };
-
-// Registers of a thread of the softmax, converting and issuing warps; the
-// sum over the four warpgroups is what the block is launched with, 4 x 128.
-template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // MN-major operand: 64 elements of N (128 bytes, swizzled) by 8 of K per
 // 1024-byte atom; atoms of the next 8 K follow, the next 64 N are lbo away.
@@ -81,15 +81,21 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -146,7 +152,7 @@ struct Walk {
 };
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
+__global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
     using C = Many<D>;
     constexpr int NQ = C::NQ, TK = C::TK;
     extern __shared__ char smem_raw[];
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
         p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
         fence_barrier_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == C::kMmaWarp) {
         __syncwarp();
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -212,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
 
     if (warp < 4 * NQ) {
         // ------------------------------------------------------ softmax
-        regs_up<NQ == 2 ? 168 : 200>();
         const int q = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tO = tmem + lanes + C::kColO + q * D;
@@ -226,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
             const size_t orow = (size_t)(w.it.rows.q0 + rowid / p.G) * p.Hq + w.it.head * p.G + rowid % p.G;
             const int pos = w.it.rows.kv - w.it.rows.n + rowid / p.G;
             float m = -INFINITY, l = 0.f;
+            f2 m2 = 0ull;                // -m twice; 0 while m is -infinity
             if (active && w.t0 < w.t1) {
                 // this row as fp16, scaled by a power of two
                 float a = 0.f, scale = 0.f;
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
                 int e = (int)(__float_as_uint(a) >> 23) - 127;
                 e = min(max(e, -100), 126);
                 const float down = bad ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
-                scale = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23) * p.scale_log2;
+                scale = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll 4
                 for (int i = 0; i < D / 8; ++i) {
                     uint4 o = make_uint4(0, 0, 0, 0);
@@ -278,73 +284,81 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
                     tc_fence_after();
                     __syncwarp();
                     const uint32_t tS = tmem + lanes + b * TK;
-                    uint32_t s[TK / 32][32];
-#pragma unroll
-                    for (int c = 0; c < TK / 32; ++c) tmem_ld_32x32b_x32(tS + 32 * c, s[c]);
-                    tmem_ld_wait();
                     const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
-                    const float4* lv = ks + TK / 4;
-                    const float4* iv = lv + TK / 4;
                     const int tok0 = t * TK;
                     // keys this row sees: columns lo .. hi - 1
-                    const int hi = p.causal ? pos + 1 - tok0 : TK;
-                    const int lo = p.window ? pos + 1 - p.window - tok0 : 0;
+                    int hi = p.causal ? pos + 1 - tok0 : TK;
+                    int lo = p.window ? pos + 1 - p.window - tok0 : 0;
                     const bool mask = __any_sync(0xffffffffu, hi < TK || lo > 0);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < TK / 4; ++c) {
-                        const float4 k4 = ks[c], b4 = lv[c];
-                        uint32_t* x = &s[c / 8][(c & 7) * 4];
-                        const f2 y0 = fma2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y));
-                        const f2 y1 = fma2(mul2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), pack2(k4.z, k4.w)), scale2, pack2(b4.z, b4.w));
-                        float2 z0 = unpack2(y0), z1 = unpack2(y1);
-                        if (mask) {
-                            z0.x = 4 * c >= lo && 4 * c < hi ? z0.x : -INFINITY;
-                            z0.y = 4 * c + 1 >= lo && 4 * c + 1 < hi ? z0.y : -INFINITY;
-                            z1.x = 4 * c + 2 >= lo && 4 * c + 2 < hi ? z1.x : -INFINITY;
-                            z1.y = 4 * c + 3 >= lo && 4 * c + 3 < hi ? z1.y : -INFINITY;
-                        }
-                        x[0] = __float_as_uint(z0.x);
-                        x[1] = __float_as_uint(z0.y);
-                        x[2] = __float_as_uint(z1.x);
-                        x[3] = __float_as_uint(z1.y);
-                        top = fmaxf(fmaxf(top, fmaxf(z0.x, z0.y)), fmaxf(z1.x, z1.y));
-                    }
-                    if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                        const float mn = fmaxf(m, top);
-                        const float f = m == mn ? 1.f : ex2(m - mn);
-                        m = mn;
-                        l *= f;
-                        if (t > w.t0) {       // the sums of the earlier tiles are in tensor memory
-                            dead = !wait(&o_done[q], cnt - 1);
-                            dead = __any_sync(0xffffffffu, dead);
-                            if (dead) break;
-                            tc_fence_after();
-                            __syncwarp();
+                    f2 l2 = pack2(0.f, 0.f);
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld_32x32b_x32(tO + 32 * c, o);
+                    for (int c = 0; c < TK / 32; ++c, ks += 8, hi -= 32, lo -= 32) {
+                        uint32_t x[32];
+                        tmem_ld_32x32b_x32(tS + 32 * c, x);
+                        tmem_ld_wait();
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 k4 = ks[i], b4 = ks[TK / 4 + i];
+                            uint32_t* y = x + 4 * i;
+                            const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y)));
+                            const float2 z1 = unpack2(fma2(mul2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(k4.z, k4.w)), scale2, pack2(b4.z, b4.w)));
+                            y[0] = __float_as_uint(z0.x);
+                            y[1] = __float_as_uint(z0.y);
+                            y[2] = __float_as_uint(z1.x);
+                            y[3] = __float_as_uint(z1.y);
+                        }
+                        if (mask) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < lo || i >= hi) x[i] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+                            const float mn = fmaxf(m, ceilf(top));
+                            const float f = m == mn ? 1.f : ex2(m - mn);
+                            m = mn;
+                            m2 = m == -INFINITY ? 0ull : pack2(-m, -m);
+                            l *= f;
+                            l2 = mul2(l2, pack2(f, f));
+                            if (t > w.t0) {       // the sums of the earlier tiles are in tensor memory
+                                dead = !wait(&o_done[q], cnt - 1);
+                                dead = __any_sync(0xffffffffu, dead);
+                                if (dead) break;
+                                tc_fence_after();
+                                __syncwarp();
+#pragma unroll 1
+                                for (int d = 0; d < D / 16; ++d) {
+                                    uint32_t o[16];
+                                    tmem_ld_32x32b_x16(tO + 16 * d, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tmem_st_32x32b_x16(tO + 16 * d, o);
+                                }
+                            }
+                            const __half2 fh = __float2half2_rn(f);
+#pragma unroll 1
+                            for (int d = 0; d < c; ++d) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(tS + 16 * d, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st_32x32b_x32(tO + 32 * c, o);
+                                for (int i = 0; i < 16; ++i) {
+                                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), fh);
+                                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                                }
+                                tmem_st_32x32b_x16(tS + 16 * d, o);
                             }
                         }
-                    }
-                    const float mm = m == -INFINITY ? 0.f : m;
-                    const f2 m2 = pack2(-mm, -mm);
-                    f2 l2 = pack2(0.f, 0.f);
+                        uint32_t ph[16];
 #pragma unroll
-                    for (int c = 0; c < TK / 64; ++c) {
-                        uint32_t ph[32];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int col = 64 * c + 4 * i;
-                            const float4 i4 = iv[col / 4];
-                            const uint32_t* x = &s[col / 32][col & 31];
-                            const float2 y0 = unpack2(add2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), m2));
-                            const float2 y1 = unpack2(add2(pack2(__uint_as_float(x[2]), __uint_as_float(x[3])), m2));
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 i4 = ks[TK / 2 + i];
+                            const uint32_t* y = x + 4 * i;
+                            const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2));
+                            const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2));
                             const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
                             l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
                             l2 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2);
@@ -352,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
                             ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
                             ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
                         }
-                        tmem_st_32x32b_x32(tS + 32 * c, ph);
+                        tmem_st_32x32b_x16(tS + 16 * c, ph);
                     }
+                    if (dead) break;
                     const float2 ls = unpack2(l2);
                     l += ls.x + ls.y;
                     tmem_st_wait();
@@ -429,36 +444,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
             }
             more = w.next(p, pl);
         }
-    } else if (warp < kMmaWarp) {
-        // ------------------------------------------------------ converters
-        if (NQ == 2) regs_down<112>();
-        else regs_down<120>();
-        const bool do_k = NQ == 2 || warp < 8, do_v = NQ == 2 || warp >= 8;
+    } else if (warp < C::kMmaWarp) {
+        // ------------------------------------------------------ keys, values
+        const bool keys = warp < C::kValueWarp;
+        const uint8_t* codes = keys ? p.k : p.v;
+        char* ring = keys ? sk : sv;
+        uint64_t* full = keys ? k_full : v_full;
+        uint64_t* empty = keys ? k_empty : v_empty;
         const int tid = threadIdx.x & 127;
         constexpr int CPR = D / 16;              // 16-byte pieces of a row
         constexpr int RPP = 128 / CPR;           // rows of a pass
         constexpr int PASSES = TK / RPP;
         const int c16 = tid % CPR, r_first = tid / CPR;
         const int page_mask = (1 << p.page_log2) - 1;
-        uint4 kr[PASSES], vr[PASSES];
+        uint4 raw[PASSES];
         float ksc = 0.f, vsc = 1.f;
         bool sc_ok = false;
         int pid = -1, tok0 = 0, kv = 0, head = 0;     // lane i: page of tokens 16 i .. of the tile, -1: none
-        auto locate = [&](int t) {
+        int t = w.t0;
+        auto settle = [&]() {                    // to the next key tile there is
+            while (more && t >= w.t1) {
+                more = w.next(p, pl);
+                t = w.t0;
+            }
+        };
+        // pages are looked up a tile before their rows are read
+        auto locate = [&]() {
             tok0 = t * TK;
             kv = w.it.rows.kv;
             head = w.it.head;
             pid = -1;
             const int tok = tok0 + 16 * lane;
-            if (lane < TK / 16 && tok < kv) {
-                pid = __ldg(p.table + (size_t)w.it.s * p.table_stride + (tok >> p.page_log2));
-                if (pid < 0 || pid >= p.n_pages) {
-                    set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
-                    pid = -1;
-                }
-            }
+            if (lane < TK / 16 && tok < kv) pid = __ldg(p.table + (size_t)w.it.s * p.table_stride + (tok >> p.page_log2));
         };
-        auto fetch = [&](uint4 (&raw)[PASSES], const uint8_t* codes) {
+        auto fetch = [&]() {
+            const int tok = tok0 + 16 * lane;
+            if (lane < TK / 16 && tok < kv && (pid < 0 || pid >= p.n_pages)) {
+                set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+                pid = -1;
+            }
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int r = r_first + i * RPP;
@@ -468,17 +492,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
                     raw[i] = ldg_stream(reinterpret_cast<const uint4*>(
                         codes + (page_row(p, pg, head) + ((tok0 + r) & page_mask)) * D + c16 * 16));
             }
-        };
-        auto fetch_scales = [&]() {
-            const int pg = __shfl_sync(0xffffffffu, pid, (tid & (TK - 1)) >> 4);
-            sc_ok = pg >= 0 && tid < TK && tok0 + tid < kv;
-            if (sc_ok) {
-                const size_t at = page_row(p, pg, head) + ((tok0 + tid) & page_mask);
-                ksc = __ldg(p.ks + at);
-                vsc = __ldg(p.vs + at);
+            if (keys) {
+                const int pg = __shfl_sync(0xffffffffu, pid, (tid & (TK - 1)) >> 4);
+                sc_ok = pg >= 0 && tid < TK && tok0 + tid < kv;
+                if (sc_ok) {
+                    const size_t at = page_row(p, pg, head) + ((tok0 + tid) & page_mask);
+                    ksc = __ldg(p.ks + at);
+                    vsc = __ldg(p.vs + at);
+                }
             }
         };
-        auto convert = [&](const uint4 (&raw)[PASSES], char* dst) {
+        settle();
+        bool have = more;                        // a tile is in the registers
+        if (have) {
+            locate();
+            fetch();
+            ++t;
+            settle();
+            if (more) locate();
+        }
+        for (uint32_t n = 0; have; ++n) {
+            const int st = n & 1;
+            const uint32_t ph = (n >> 1) ^ 1;
+            bool dead = !wait(&empty[st], ph) || (keys && !wait(&sc_free[st], ph));
+            dead = __any_sync(0xffffffffu, dead);
+            if (dead) break;
+            if (keys && tid < TK) {
+                // a place without a token weighs nothing; a scale that is no
+                // positive number makes its token's scores NaN
+                float* sc = ssc + st * (C::kScaleBytes / 4) + tid;
+                const bool fine = vsc > 0.f && vsc < INFINITY;
+                sc[0] = sc_ok ? ksc * p.scale_log2 : 0.f;
+                sc[TK] = !sc_ok ? -INFINITY : fine ? __log2f(vsc) : __int_as_float(0x7fffffff);
+                sc[2 * TK] = sc_ok && fine ? __frcp_rn(vsc) : 1.f;
+            }
+            char* dst = ring + st * C::kOpBytes + (c16 >> 2) * (TK * 128);
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int r = r_first + i * RPP;
@@ -486,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
                 uint32_t h[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) codes_to_f16<FMT>(biased<FMT>(u[j]), h[2 * j], h[2 * j + 1]);
-                char* d = dst + (c16 >> 2) * (TK * 128) + r * 128;
+                char* d = dst + r * 128;
                 // pieces of the second 64 columns write their halves in the
                 // other order: eight lanes then cover all banks
                 const int sw = (c16 >> 2) & 1, c0 = 2 * (c16 & 3);
@@ -496,62 +544,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
             }
             fence_proxy_async_smem();
             __syncwarp();
-        };
-        int t = w.t0;
-        auto settle = [&]() {                    // to the next key tile there is
-            while (more && t >= w.t1) {
-                more = w.next(p, pl);
-                t = w.t0;
+            if (lane == 0) mbar_arrive(&full[st]);
+            have = more;
+            if (have) {
+                fetch();
+                ++t;
+                settle();
+                if (more) locate();
             }
-        };
-        settle();
-        if (more) {
-            locate(t);
-            if (do_k) { fetch(kr, p.k); fetch_scales(); }
-            if (do_v) fetch(vr, p.v);
-        }
-        uint32_t n = 0;
-        while (more) {
-            const int st = n & 1;
-            const uint32_t ph = (n >> 1) ^ 1;
-            bool dead = false;
-            if (do_k) {
-                dead = !wait(&sc_free[st], ph) || !wait(&k_empty[st], ph);
-                dead = __any_sync(0xffffffffu, dead);
-                if (dead) break;
-                if (tid < TK) {
-                    // a place without a token weighs nothing; a scale that is
-                    // no positive number makes its token's scores NaN
-                    float* sc = ssc + st * (C::kScaleBytes / 4) + tid;
-                    const bool fine = vsc > 0.f && vsc < INFINITY;
-                    sc[0] = sc_ok ? ksc : 0.f;
-                    sc[TK] = !sc_ok ? -INFINITY : fine ? __log2f(vsc) : __int_as_float(0x7fffffff);
-                    sc[2 * TK] = sc_ok && fine ? __frcp_rn(vsc) : 1.f;
-                }
-                convert(kr, sk + st * C::kOpBytes);
-                if (lane == 0) mbar_arrive(&k_full[st]);
-            }
-            ++t;
-            settle();
-            if (more) {
-                locate(t);
-                if (do_k) { fetch(kr, p.k); fetch_scales(); }
-            }
-            if (do_v) {
-                dead = !wait(&v_empty[st], ph);
-                dead = __any_sync(0xffffffffu, dead);
-                if (dead) break;
-                convert(vr, sv + st * C::kOpBytes);
-                if (lane == 0) mbar_arrive(&v_full[st]);
-                if (more) fetch(vr, p.v);
-            }
-            ++n;
         }
     } else {
         // ------------------------------------------------------ issue
-        if (NQ == 2) regs_down<64>();
-        else regs_down<72>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (lane == 0) {
             const uint32_t idesc_s = idesc_f16(128, TK, 0), idesc_o = idesc_f16(128, D, 0) | kTransposeB;
             const uint32_t q_base = smem_u32(sq), k_base = smem_u32(sk), v_base = smem_u32(sv);
             auto scores = [&](int q, int b, int st) {
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attend_many(AttendParams p, Pla
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == C::kMmaWarp) {
         tc_fence_after();
         __syncwarp();
         tmem_dealloc(tmem, 512);
@@ -647,7 +651,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t st) {
     const Plan pl{C::kRows, D == 256 ? 6 : 7, 1};
     cudaError_t e = allow_smem<k_attend_many<D, FMT>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    k_attend_many<D, FMT><<<kSms, kThreads, C::kSmem, st>>>(p, pl);
+    k_attend_many<D, FMT><<<kSms, C::kThreads, C::kSmem, st>>>(p, pl);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_join(p, C::kRows, kSms, false, st);
