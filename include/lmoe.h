@@ -401,7 +401,8 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  *        (-inf for a row without keys), for joining parts of a context
  * Products are of the bf16 queries and the stored codes as fp16, exact, with
  * fp32 sums; the probabilities (times the value's scale) are rounded to
- * fp16.  Results do not depend on timing.
+ * fp16.  The scales of the value rows that one query sees may lie up to
+ * 2^100 apart.  Results do not depend on timing.
  * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that
  * is not finite), _UNSUPPORTED, _WORKSPACE; n_tokens = 0 or n_seqs = 0
  * launches nothing. */

@@ -8,7 +8,7 @@
 //   t_j = scale log2(e) a_j (q . ck_j) + log2(b_j),   p_j = 2^(t_j - m),
 //   out = sum_j p_j cv_j / sum_j p_j (1 / b_j).
 // Folding the value's scale into the exponent keeps the second product in
-// fp16 whatever the scales are: p is at most 2^8 (below) and the codes are
+// fp16 whatever the scales are: p is at most 2^14 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
 // that of p to fp16 (half a step, 2^-12).  Queries are scaled by a power of
 // two per row into the fp16 range, which is exact; sums are fp32.
@@ -309,15 +309,14 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
 #pragma unroll
                         for (int i = 0; i < C::kVw; ++i) vw[h][i] = 0u;
             }
-            // the running maximum is raised only when a score passes it by 8:
-            // p stays below 2^8, far inside fp16, and most steps skip the
-            // exchange between lanes and the rescaling
+            // m is raised rarely, so most steps skip the exchange between
+            // lanes and the rescaling
 #pragma unroll
             for (int r = 0; r < NR; ++r)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     top = fmaxf(s[r][i], s[r][i + 2]);
-                    grow |= top > m[r][i] + 8.f;
+                    grow |= top > m[r][i] + kMaxP;
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 4));
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16));
-                        n = fmaxf(n, m[r][i]);
+                        n = fmaxf(n - kRaiseP, m[r][i]);
                         const float f = m[r][i] == n ? 1.f : ex2(m[r][i] - n);
                         m[r][i] = n;
                         l[r][i] *= f;

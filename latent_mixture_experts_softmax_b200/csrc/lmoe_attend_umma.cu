@@ -19,10 +19,10 @@
 //                transposed.
 //   issue        one thread: S = Q K^T and O += P V
 // With two query tiles the softmax of one runs beside the products of the
-// other; with one, two score buffers let the next S run ahead.  The row
-// maximum is raised only when a score passes it by 2^8 (p stays far inside
-// fp16), and to a whole number, so that what it rescales (O, and the P of the
-// tile's earlier pieces) changes by a power of two: the scores are gone
+// other; with one, two score buffers let the next S run ahead.  The row's
+// reference m is raised as in the kernel for few rows, and to a whole number,
+// so that what it rescales (O, and the P of the tile's earlier pieces)
+// changes by a power of two: the scores are gone
 // through once, and the loop stays small enough for the instruction caches
 // (a form that held a tile's scores in registers, unrolled, spent a third of
 // its time waiting for instructions).
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
     using C = Many<D>;
     constexpr int NQ = C::NQ, TK = C::TK;
     extern __shared__ char smem_raw[];
-    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
     char* sq = smem;
     char* sk = sq + NQ * C::kQBytes;
     char* sv = sk + 2 * C::kOpBytes;
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
                         }
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                        if (__any_sync(0xffffffffu, top > m + 8.f)) {
-                            const float mn = fmaxf(m, ceilf(top));
+                        if (__any_sync(0xffffffffu, top > m + kMaxP)) {
+                            const float mn = fmaxf(m, ceilf(top) - kRaiseP);
                             const float f = m == mn ? 1.f : ex2(m - mn);
                             m = mn;
                             m2 = m == -INFINITY ? 0ull : pack2(-m, -m);
@@ -452,10 +452,12 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
         uint64_t* full = keys ? k_full : v_full;
         uint64_t* empty = keys ? k_empty : v_empty;
         const int tid = threadIdx.x & 127;
-        constexpr int CPR = D / 16;              // 16-byte pieces of a row
-        constexpr int RPP = 128 / CPR;           // rows of a pass
+        // eight lanes: four 16-byte pieces of two rows, whose swizzled places
+        // then cover all banks
+        constexpr int BLKS = D / 64;             // 64-column blocks of a row
+        constexpr int RPP = 32 / BLKS;           // rows of a pass
         constexpr int PASSES = TK / RPP;
-        const int c16 = tid % CPR, r_first = tid / CPR;
+        const int c4 = tid & 3, blk = (tid >> 3) % BLKS, r_first = (tid >> 3) / BLKS * 2 + ((tid >> 2) & 1);
         const int page_mask = (1 << p.page_log2) - 1;
         uint4 raw[PASSES];
         float ksc = 0.f, vsc = 1.f;
@@ -479,26 +481,27 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
         };
         auto fetch = [&]() {
             const int tok = tok0 + 16 * lane;
-            if (lane < TK / 16 && tok < kv && (pid < 0 || pid >= p.n_pages)) {
-                set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
-                pid = -1;
+            long long at = -1;                   // lane i: first row of tokens 16 i .. in the scale arrays
+            if (lane < TK / 16 && tok < kv) {
+                if (pid < 0 || pid >= p.n_pages) set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+                else at = (long long)page_row(p, pid, head) + (tok & page_mask);
             }
+            const int there = kv - tok0;         // rows of the tile that hold a token
+            const uint8_t* src = codes + r_first % 16 * D + blk * 64 + c4 * 16;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int r = r_first + i * RPP;
-                const int pg = __shfl_sync(0xffffffffu, pid, r >> 4);
+                const long long row = __shfl_sync(0xffffffffu, at, RPP >= 16 ? r >> 4 : i * RPP >> 4);
                 raw[i] = make_uint4(0, 0, 0, 0);
-                if (pg >= 0 && tok0 + r < kv)
-                    raw[i] = ldg_stream(reinterpret_cast<const uint4*>(
-                        codes + (page_row(p, pg, head) + ((tok0 + r) & page_mask)) * D + c16 * 16));
+                if (row >= 0 && r < there)
+                    raw[i] = ldg_stream(reinterpret_cast<const uint4*>(src + row * D + (i * RPP % 16) * D));
             }
             if (keys) {
-                const int pg = __shfl_sync(0xffffffffu, pid, (tid & (TK - 1)) >> 4);
-                sc_ok = pg >= 0 && tid < TK && tok0 + tid < kv;
+                const long long row = __shfl_sync(0xffffffffu, at, (tid & (TK - 1)) >> 4);
+                sc_ok = row >= 0 && tid < TK && tid < there;
                 if (sc_ok) {
-                    const size_t at = page_row(p, pg, head) + ((tok0 + tid) & page_mask);
-                    ksc = __ldg(p.ks + at);
-                    vsc = __ldg(p.vs + at);
+                    ksc = __ldg(p.ks + row + (tid & 15));
+                    vsc = __ldg(p.vs + row + (tid & 15));
                 }
             }
         };
@@ -526,21 +529,17 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
                 sc[TK] = !sc_ok ? -INFINITY : fine ? __log2f(vsc) : __int_as_float(0x7fffffff);
                 sc[2 * TK] = sc_ok && fine ? __frcp_rn(vsc) : 1.f;
             }
-            char* dst = ring + st * C::kOpBytes + (c16 >> 2) * (TK * 128);
+            char* dst = ring + st * C::kOpBytes + blk * (TK * 128) + r_first * 128;
+            const int o0 = ((2 * c4) ^ (r_first & 7)) << 4;     // (a pass is a multiple of eight rows)
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
-                const int r = r_first + i * RPP;
                 const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) codes_to_f16<FMT>(biased<FMT>(u[j]), h[2 * j], h[2 * j + 1]);
-                char* d = dst + r * 128;
-                // pieces of the second 64 columns write their halves in the
-                // other order: eight lanes then cover all banks
-                const int sw = (c16 >> 2) & 1, c0 = 2 * (c16 & 3);
-                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4*>(d + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? b : a;
-                *reinterpret_cast<uint4*>(d + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? a : b;
+                char* d = dst + i * RPP * 128;
+                *reinterpret_cast<uint4*>(d + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(d + (o0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
             fence_proxy_async_smem();
             __syncwarp();
