@@ -585,14 +585,20 @@ cudaError_t launch_rows(const AttendParams& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t attend_ws_bytes(int D) {
+static size_t parts_bytes(int D) {
     const size_t few = kMaxCtas * part_floats(kFewRows, D), many = kSms * part_floats(many_rows(D), D);
-    return kCutBytes + 2 * 4 * (few > many ? few : many);
+    return (2 * 4 * (few > many ? few : many) + 255) & ~(size_t)255;
 }
+
+size_t attend_ws_bytes(int D) { return kCutBytes + parts_bytes(D) + kImageBytes; }
 
 cudaError_t run_attend(AttendParams p, void* ws, cudaStream_t st) {
     p.cuts = static_cast<int4*>(ws);
     p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes);
+    p.img = static_cast<char*>(ws) + kCutBytes + parts_bytes(p.D);
+    p.img_tiles = 0;
+    p.h0 = 0;
+    p.Hn = p.Hk;
     const bool i8 = p.fmt == LMOE_KV_INT8;
     if (p.D == 64) return i8 ? launch_rows<64, LMOE_KV_INT8>(p, st) : launch_rows<64, LMOE_KV_E4M3>(p, st);
     if (p.D == 128) return i8 ? launch_rows<128, LMOE_KV_INT8>(p, st) : launch_rows<128, LMOE_KV_E4M3>(p, st);

@@ -96,7 +96,7 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
     const int per = (p.n_seqs + nt - 1) / nt;
     const int a = (int)min((long long)p.n_seqs, (long long)threadIdx.x * per), b = min(p.n_seqs, a + per);
     long long mine = 0;
-    for (int i = 0; i < per; ++i) mine += lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hk;
+    for (int i = 0; i < per; ++i) mine += lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hn;
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -117,7 +117,7 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
     const long long x = x_of(l);
     if (__any_sync(0xffffffffu, x >= before && x < before + mine)) {
         for (int i = 0; i < per; ++i) {
-            const long long u = lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hk;
+            const long long u = lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hn;
             if (x >= before && x < before + u) {
                 s_seq = a + i;
                 s_base = before;
@@ -146,8 +146,9 @@ struct Item {
         if (s >= p.n_seqs) return false;
         rows = seq_rows(p, s);
         const long long per_head = head_units(p, pl, rows);
-        head = (int)((x - base) / per_head);
-        begin = base + head * per_head;
+        const int h = (int)((x - base) / per_head);
+        head = p.h0 + h;
+        begin = base + h * per_head;
         const int n = n_row_tiles(p, pl, rows), lane = threadIdx.x & 31;
         for (rt = 0;; rt += 32) {
             const long long u = rt + lane < n ? tile_of(p, pl, rows, rt + lane).units : 0;
@@ -174,8 +175,8 @@ struct Item {
         begin += tile.units;
         if (++rt >= n_row_tiles(p, pl, rows)) {
             rt = 0;
-            if (++head >= p.Hk) {
-                head = 0;
+            if (++head >= p.h0 + p.Hn) {
+                head = p.h0;
                 do {
                     if (++s >= p.n_seqs) return false;
                     rows = seq_rows(p, s);
@@ -236,6 +237,13 @@ __device__ __forceinline__ uint32_t biased(uint32_t w) { return FMT == LMOE_KV_I
 // Query rows of an item of the kernel for many rows: two tensor-core tiles of
 // 128, or one where the accumulators of one fill tensor memory's half.
 __host__ __device__ constexpr int many_rows(int D) { return D == 256 ? 128 : 256; }
+
+// Images of key tiles: tokens of a tile, bytes (keys and values in fp16, three
+// floats a token), and what a workspace holds of them: half of L2.
+__host__ __device__ constexpr int image_tokens(int D) { return D == 256 ? 64 : 128; }
+__host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12); }
+constexpr size_t kImageBytes = 64u << 20;
+constexpr int kImageRowTiles = 4;       // images are made for more row tiles than this
 
 constexpr size_t kCutBytes = 8192;      // kMaxCtas records of 16 bytes
 static_assert(kMaxCtas * 16 <= kCutBytes, "cut records");

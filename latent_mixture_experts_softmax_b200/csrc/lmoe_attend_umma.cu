@@ -41,17 +41,20 @@ using namespace sm100;
 using namespace attend;
 
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
+constexpr uint64_t kDrainLimit = 20000000ull;    // and per wait for a copy in flight after one gave up
 
-template <int D>
+template <int D, bool IMG>
 struct Many {
     static constexpr int NQ = D == 256 ? 1 : 2;       // query tiles of 128 rows
     static constexpr int TK = D == 256 ? 64 : 128;    // tokens of a key tile
     static constexpr int kRows = NQ * 128;
-    static constexpr int kKeyWarp = 4 * NQ, kValueWarp = kKeyWarp + 4, kMmaWarp = kValueWarp + 4;
+    static constexpr int kKeyWarp = 4 * NQ, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
+                         kMmaWarp = kValueWarp + (IMG ? 0 : 4);
     static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
+    static constexpr size_t kImage = 2 * kOpBytes + kScaleBytes;   // keys, values, scales of a tile
     static constexpr size_t kSmem = 1024 + NQ * kQBytes + 4 * kOpBytes + 2 * kScaleBytes + 256;
     static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 (b * TK), sums from 256 (q * D)
 };
@@ -100,6 +103,14 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Contiguous bytes (16-byte aligned, a multiple of 16) to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Pairs of fp32 in one instruction.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -128,6 +139,15 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     return r;
 }
 
+// What the softmax needs of a token.  A place without one weighs nothing; a
+// value scale that is no positive number makes its token's scores NaN.
+__device__ __forceinline__ void token_scales(const AttendParams& p, bool some, float ks, float vs, float* sc, int TK) {
+    const bool fine = vs > 0.f && vs < INFINITY;
+    sc[0] = some ? ks * p.scale_log2 : 0.f;
+    sc[TK] = !some ? -INFINITY : fine ? __log2f(vs) : __int_as_float(0x7fffffff);
+    sc[2 * TK] = some && fine ? __frcp_rn(vs) : 1.f;
+}
+
 // The CTA's piece of the line, item by item.
 struct Walk {
     Item it;
@@ -151,9 +171,9 @@ struct Walk {
     }
 };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
-    using C = Many<D>;
+template <int D, int FMT, bool IMG>
+__global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
+    using C = Many<D, IMG>;
     constexpr int NQ = C::NQ, TK = C::TK;
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
@@ -178,8 +198,8 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&k_full[i], 4);
-            mbar_init(&v_full[i], 4);
+            mbar_init(&k_full[i], IMG ? 1 : 4);
+            mbar_init(&v_full[i], IMG ? 1 : 4);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
@@ -444,7 +464,41 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
             }
             more = w.next(p, pl);
         }
-    } else if (warp < C::kMmaWarp) {
+    } else if (IMG && warp < C::kMmaWarp) {
+        // ------------------------------------------------------ images
+        if (lane == 0) {
+            uint32_t n = 0;
+            bool dead = false, half = false;     // half: only the keys of tile n are on their way
+            while (more && !dead) {
+                const char* img = p.img + ((size_t)w.it.s * p.Hn + (w.it.head - p.h0)) * p.img_tiles * C::kImage;
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const char* src = img + (size_t)t * C::kImage;
+                    const int st = n & 1;
+                    const uint32_t ph = (n >> 1) ^ 1;
+                    dead = !wait(&sc_free[st], ph) || !wait(&k_empty[st], ph);
+                    if (dead) break;
+                    mbar_arrive_expect_tx(&k_full[st], (uint32_t)(C::kOpBytes + C::kScaleBytes));
+                    bulk_load(sk + st * C::kOpBytes, src, (uint32_t)C::kOpBytes, &k_full[st]);
+                    bulk_load(ssc + st * (C::kScaleBytes / 4), src + 2 * C::kOpBytes, (uint32_t)C::kScaleBytes, &k_full[st]);
+                    half = true;
+                    dead = !wait(&v_empty[st], ph);
+                    if (dead) break;
+                    half = false;
+                    mbar_arrive_expect_tx(&v_full[st], (uint32_t)C::kOpBytes);
+                    bulk_load(sv + st * C::kOpBytes, src + C::kOpBytes, (uint32_t)C::kOpBytes, &v_full[st]);
+                }
+                if (!dead) more = w.next(p, pl);
+            }
+            // the copies in flight end before the CTA does, after an abort too
+            volatile int no_abort = 0;
+            for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) {
+                mbar_wait(&k_full[i & 1], (i >> 1) & 1, &no_abort, kDrainLimit);
+                mbar_wait(&v_full[i & 1], (i >> 1) & 1, &no_abort, kDrainLimit);
+            }
+            if (half) mbar_wait(&k_full[n & 1], (n >> 1) & 1, &no_abort, kDrainLimit);
+        }
+        __syncwarp();
+    } else if (!IMG && warp < C::kMmaWarp) {
         // ------------------------------------------------------ keys, values
         const bool keys = warp < C::kValueWarp;
         const uint8_t* codes = keys ? p.k : p.v;
@@ -459,10 +513,13 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
         constexpr int PASSES = TK / RPP;
         const int c4 = tid & 3, blk = (tid >> 3) % BLKS, r_first = (tid >> 3) / BLKS * 2 + ((tid >> 2) & 1);
         const int page_mask = (1 << p.page_log2) - 1;
-        uint4 raw[PASSES];
-        float ksc = 0.f, vsc = 1.f;
-        bool sc_ok = false;
-        int pid = -1, tok0 = 0, kv = 0, head = 0;     // lane i: page of tokens 16 i .. of the tile, -1: none
+        struct Raw {
+            uint4 v[PASSES];
+            float ksc, vsc;
+            uint32_t none;                       // bit i: row i of this thread holds no token, bit 31: its scales
+        };
+        uint32_t pid = ~0u;                      // lane i: page of tokens 16 i .. of the next tile
+        int tok0 = 0, there = 0, head = 0;       // its first token, rows that hold a token (0: no such tile)
         int t = w.t0;
         auto settle = [&]() {                    // to the next key tile there is
             while (more && t >= w.t1) {
@@ -473,67 +530,69 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
         // pages are looked up a tile before their rows are read
         auto locate = [&]() {
             tok0 = t * TK;
-            kv = w.it.rows.kv;
+            there = more ? min(w.it.rows.kv - tok0, TK) : 0;
             head = w.it.head;
-            pid = -1;
-            const int tok = tok0 + 16 * lane;
-            if (lane < TK / 16 && tok < kv) pid = __ldg(p.table + (size_t)w.it.s * p.table_stride + (tok >> p.page_log2));
+            // (lanes past the last token look up the tile's first page)
+            pid = more ? __ldg(p.table + (size_t)w.it.s * p.table_stride +
+                               ((tok0 + (16 * lane < there ? 16 * lane : 0)) >> p.page_log2)) : 0;
         };
-        auto fetch = [&]() {
-            const int tok = tok0 + 16 * lane;
+        // Every load has a place to read: one that is not due reads the
+        // cache's first row, and its result is dropped.  (Under a condition
+        // the compiler waits for each load before it issues the next.)
+        auto fetch = [&](Raw& raw) {
             long long at = -1;                   // lane i: first row of tokens 16 i .. in the scale arrays
-            if (lane < TK / 16 && tok < kv) {
-                if (pid < 0 || pid >= p.n_pages) set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
-                else at = (long long)page_row(p, pid, head) + (tok & page_mask);
+            if (16 * lane < there) {
+                if (pid >= (uint32_t)p.n_pages) set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+                else at = (long long)page_row(p, (int)pid, head) + ((tok0 + 16 * lane) & page_mask);
             }
-            const int there = kv - tok0;         // rows of the tile that hold a token
-            const uint8_t* src = codes + r_first % 16 * D + blk * 64 + c4 * 16;
+            const uint8_t* src = codes + blk * 64 + c4 * 16;
+            raw.none = 0;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int r = r_first + i * RPP;
-                const long long row = __shfl_sync(0xffffffffu, at, RPP >= 16 ? r >> 4 : i * RPP >> 4);
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (row >= 0 && r < there)
-                    raw[i] = ldg_stream(reinterpret_cast<const uint4*>(src + row * D + (i * RPP % 16) * D));
+                const long long first = __shfl_sync(0xffffffffu, at, RPP >= 16 ? r >> 4 : i * RPP >> 4);
+                const bool good = first >= 0 && r < there;
+                raw.none |= good ? 0u : 1u << i;
+                raw.v[i] = ldg_stream(reinterpret_cast<const uint4*>(src + (good ? (first + (r & 15)) * D : 0ll)));
             }
-            if (keys) {
-                const long long row = __shfl_sync(0xffffffffu, at, (tid & (TK - 1)) >> 4);
-                sc_ok = row >= 0 && tid < TK && tid < there;
-                if (sc_ok) {
-                    ksc = __ldg(p.ks + row + (tid & 15));
-                    vsc = __ldg(p.vs + row + (tid & 15));
-                }
-            }
+            const long long first = __shfl_sync(0xffffffffu, at, (tid & (TK - 1)) >> 4);
+            const bool good = keys && first >= 0 && tid < there;
+            raw.none |= good ? 0u : 1u << 31;
+            raw.ksc = __ldg(p.ks + (good ? first + (tid & 15) : 0ll));
+            raw.vsc = __ldg(p.vs + (good ? first + (tid & 15) : 0ll));
         };
+        Raw cur;
         settle();
-        bool have = more;                        // a tile is in the registers
-        if (have) {
-            locate();
-            fetch();
+        bool have = more;                        // a tile is on its way to `cur`
+        locate();
+        fetch(cur);
+        ++t;
+        settle();
+        locate();
+        for (uint32_t n = 0; have; ++n) {
+            Raw next;                            // (a copy, whose moves wait for the loads at the end of the pass)
+            have = more;
+            fetch(next);
             ++t;
             settle();
-            if (more) locate();
-        }
-        for (uint32_t n = 0; have; ++n) {
+            locate();
             const int st = n & 1;
             const uint32_t ph = (n >> 1) ^ 1;
             bool dead = !wait(&empty[st], ph) || (keys && !wait(&sc_free[st], ph));
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
-            if (keys && tid < TK) {
-                // a place without a token weighs nothing; a scale that is no
-                // positive number makes its token's scores NaN
-                float* sc = ssc + st * (C::kScaleBytes / 4) + tid;
-                const bool fine = vsc > 0.f && vsc < INFINITY;
-                sc[0] = sc_ok ? ksc * p.scale_log2 : 0.f;
-                sc[TK] = !sc_ok ? -INFINITY : fine ? __log2f(vsc) : __int_as_float(0x7fffffff);
-                sc[2 * TK] = sc_ok && fine ? __frcp_rn(vsc) : 1.f;
+            if (keys && tid < TK)
+                token_scales(p, !(cur.none >> 31), cur.ksc, cur.vsc, ssc + st * (C::kScaleBytes / 4) + tid, TK);
+            if (cur.none << 1) {                 // codes behind the last token may be anything, a NaN code too
+#pragma unroll
+                for (int i = 0; i < PASSES; ++i)
+                    if (cur.none >> i & 1) cur.v[i] = make_uint4(0, 0, 0, 0);
             }
             char* dst = ring + st * C::kOpBytes + blk * (TK * 128) + r_first * 128;
             const int o0 = ((2 * c4) ^ (r_first & 7)) << 4;     // (a pass is a multiple of eight rows)
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
-                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                const uint32_t u[4] = {cur.v[i].x, cur.v[i].y, cur.v[i].z, cur.v[i].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) codes_to_f16<FMT>(biased<FMT>(u[j]), h[2 * j], h[2 * j + 1]);
@@ -544,13 +603,7 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
-            have = more;
-            if (have) {
-                fetch();
-                ++t;
-                settle();
-                if (more) locate();
-            }
+            cur = next;
         }
     } else {
         // ------------------------------------------------------ issue
@@ -643,26 +696,117 @@ __global__ void __launch_bounds__(Many<D>::kThreads, 1) k_attend_many(AttendPara
     if (threadIdx.x == 0 && *abort_flag) set_status(p.ctrl, LMOE_ERR_TIMEOUT);
 }
 
+// ---------------------------------------------------------------------------
+// images
+// ---------------------------------------------------------------------------
+
+// Block (tile, head, sequence): the shared-memory image of a key tile -- keys
+// and values as swizzled fp16 operands, then per token key scale times
+// softmax scale, log2 and inverse of the value scale -- as the key and value
+// warps above write it.
 template <int D, int FMT>
+__global__ void __launch_bounds__(256) k_attend_images(AttendParams p) {
+    using C = Many<D, true>;
+    constexpr int TK = C::TK, BLKS = D / 64, RPP = 64 / BLKS;      // rows of a pass
+    const SeqRows r = seq_rows(p, blockIdx.z);
+    if (r.n <= 0) return;
+    const int first = r.kv - r.n, lo = p.window ? max(0, first - p.window + 1) : 0;
+    const int tok0 = blockIdx.x * TK;
+    if (tok0 >= r.kv || tok0 + TK <= lo) return;
+    const int head = p.h0 + blockIdx.y;
+    char* img = p.img + (((size_t)blockIdx.z * p.Hn + blockIdx.y) * p.img_tiles + blockIdx.x) * C::kImage;
+    const int32_t* table = p.table + (size_t)blockIdx.z * p.table_stride;
+    const int page_mask = (1 << p.page_log2) - 1;
+    const int c4 = threadIdx.x & 3, blk = (threadIdx.x >> 3) % BLKS;
+    const int r_first = (threadIdx.x >> 3) / BLKS * 2 + ((threadIdx.x >> 2) & 1);
+    auto place = [&](int tok) -> long long {                       // row in the scale arrays; -1: none
+        if (tok >= r.kv) return -1;
+        const int page = __ldg(table + (tok >> p.page_log2));
+        if (page < 0 || page >= p.n_pages) {
+            set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+            return -1;
+        }
+        return (long long)page_row(p, page, head) + (tok & page_mask);
+    };
+#pragma unroll
+    for (int i = 0; i < TK / RPP; ++i) {
+        const int row = r_first + i * RPP;
+        const long long at = place(tok0 + row);
+        uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (at >= 0) {
+            raw[0] = ldg_stream(reinterpret_cast<const uint4*>(p.k + at * D + blk * 64 + c4 * 16));
+            raw[1] = ldg_stream(reinterpret_cast<const uint4*>(p.v + at * D + blk * 64 + c4 * 16));
+        }
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            const uint32_t u[4] = {raw[o].x, raw[o].y, raw[o].z, raw[o].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) codes_to_f16<FMT>(biased<FMT>(u[j]), h[2 * j], h[2 * j + 1]);
+            char* d = img + o * C::kOpBytes + blk * (TK * 128) + row * 128;
+            const int o0 = ((2 * c4) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(d + o0) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(d + (o0 ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+    }
+    if (threadIdx.x < TK) {
+        const long long at = place(tok0 + threadIdx.x);
+        token_scales(p, at >= 0, at >= 0 ? __ldg(p.ks + at) : 0.f, at >= 0 ? __ldg(p.vs + at) : 0.f,
+                     reinterpret_cast<float*>(img + 2 * C::kOpBytes) + threadIdx.x, TK);
+    }
+}
+
+template <int D, int FMT, bool IMG>
 cudaError_t launch(const AttendParams& p, cudaStream_t st) {
-    using C = Many<D>;
-    static_assert(C::kRows == many_rows(D), "rows of an item");
+    using C = Many<D, IMG>;
+    static_assert(C::kRows == many_rows(D) && C::kImage == image_bytes(D) && C::TK == image_tokens(D), "sizes");
     const Plan pl{C::kRows, D == 256 ? 6 : 7, 1};
-    cudaError_t e = allow_smem<k_attend_many<D, FMT>>(C::kSmem);
+    cudaError_t e = allow_smem<k_attend_many<D, FMT, IMG>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    k_attend_many<D, FMT><<<kSms, C::kThreads, C::kSmem, st>>>(p, pl);
+    k_attend_many<D, FMT, IMG><<<kSms, C::kThreads, C::kSmem, st>>>(p, pl);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_join(p, C::kRows, kSms, false, st);
+}
+
+// Images pay where several row tiles read a key tile, and go in groups of
+// sequences, or of heads of one sequence, that fit the workspace (and L2).  A
+// sequence that may be too long for them, even one head of it, is converted
+// on the way.
+template <int D, int FMT>
+cudaError_t launch_groups(AttendParams p, cudaStream_t st) {
+    const long long tiles = (((long long)p.table_stride << p.page_log2) + image_tokens(D) - 1) / image_tokens(D);
+    const long long fit = (long long)(kImageBytes / image_bytes(D)) / tiles;      // (sequence, head) pairs of a group
+    if ((long long)p.max_new * p.G <= kImageRowTiles * many_rows(D) || fit < 1) return launch<D, FMT, false>(p, st);
+    const int heads = (int)(fit < p.Hk ? fit : p.Hk);
+    const int seqs = (int)(fit / heads < p.n_seqs ? fit / heads : p.n_seqs);
+    AttendParams g = p;
+    g.img_tiles = (int)tiles;
+    for (int s = 0; s < p.n_seqs; s += seqs) {
+        g.n_seqs = p.n_seqs - s < seqs ? p.n_seqs - s : seqs;
+        g.q_start = p.q_start + s;
+        g.kv_len = p.kv_len + s;
+        g.table = p.table + (size_t)s * p.table_stride;
+        for (int h = 0; h < p.Hk; h += heads) {
+            g.h0 = h;
+            g.Hn = p.Hk - h < heads ? p.Hk - h : heads;
+            // (a grid's y and z end at 65535; fit is far below)
+            k_attend_images<D, FMT><<<dim3((unsigned)tiles, g.Hn, g.n_seqs), 256, 0, st>>>(g);
+            cudaError_t e = cudaGetLastError();
+            if (e == cudaSuccess) e = launch<D, FMT, true>(g, st);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t attend::launch_many(const AttendParams& p, cudaStream_t st) {
     const bool i8 = p.fmt == LMOE_KV_INT8;
-    if (p.D == 64) return i8 ? launch<64, LMOE_KV_INT8>(p, st) : launch<64, LMOE_KV_E4M3>(p, st);
-    if (p.D == 128) return i8 ? launch<128, LMOE_KV_INT8>(p, st) : launch<128, LMOE_KV_E4M3>(p, st);
-    return i8 ? launch<256, LMOE_KV_INT8>(p, st) : launch<256, LMOE_KV_E4M3>(p, st);
+    if (p.D == 64) return i8 ? launch_groups<64, LMOE_KV_INT8>(p, st) : launch_groups<64, LMOE_KV_E4M3>(p, st);
+    if (p.D == 128) return i8 ? launch_groups<128, LMOE_KV_INT8>(p, st) : launch_groups<128, LMOE_KV_E4M3>(p, st);
+    return i8 ? launch_groups<256, LMOE_KV_INT8>(p, st) : launch_groups<256, LMOE_KV_E4M3>(p, st);
 }
 
 }  // namespace lmoe

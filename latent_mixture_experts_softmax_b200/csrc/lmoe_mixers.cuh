@@ -78,6 +78,9 @@ struct AttendParams : KvParams {
     float* lse;
     int4* cuts;            // per CTA: the item it began and others go on with
     float* part;           // parts of items cut between CTAs
+    int h0, Hn;            // key heads of this launch
+    char* img;             // images of key tiles [sequence][head of the launch][tile]
+    int img_tiles;
 };
 
 struct DeltaParams {
