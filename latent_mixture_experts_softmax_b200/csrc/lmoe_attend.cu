@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
         return;
     }
     Item it;
-    it.seek(p, pl, line.seq, line.base, x);
+    it.seek(p, pl, line, x);
     const int page_mask = (1 << p.page_log2) - 1;
 
     for (;;) {
@@ -564,7 +564,7 @@ namespace {
 template <int D, int FMT, int NR, int NS>
 cudaError_t launch_few(const AttendParams& p, cudaStream_t st) {
     using C = Few<D, FMT, NR, NS>;
-    const Plan pl{C::kRows, 4, C::kGroups};
+    const Plan pl{C::kRows, 4, C::kGroups, 0};
     constexpr int kCtas = kSms * C::kCtasPerSm;
     cudaError_t e = allow_smem<k_attend_few<D, FMT, NR, NS>>(C::kSmem);
     if (e != cudaSuccess) return e;

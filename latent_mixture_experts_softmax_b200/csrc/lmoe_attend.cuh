@@ -24,6 +24,7 @@ struct Plan {
     int rows;          // query rows of a row tile
     int step_log2;     // tokens of a step
     int groups;        // steps of a unit
+    int extra;         // units of a row tile besides those of its steps
 };
 
 struct Tile {
@@ -43,7 +44,7 @@ __device__ __forceinline__ Tile tile_of(const AttendParams& p, const Plan& pl, c
     Tile t;
     t.step0 = lo >> pl.step_log2;
     t.step1 = hi > lo ? ((hi - 1) >> pl.step_log2) + 1 : t.step0;
-    t.units = max(1, (t.step1 - t.step0 + pl.groups - 1) / pl.groups);
+    t.units = max(1, (t.step1 - t.step0 + pl.groups - 1) / pl.groups) + pl.extra;
     return t;
 }
 
@@ -80,8 +81,8 @@ __device__ __forceinline__ long long lane_units(const AttendParams& p, const Pla
 
 struct Line {
     long long total, chunk;   // units, and units per CTA
-    int seq;                  // the sequence holding unit x, and its first unit
-    long long base;
+    int seq;                  // the sequence holding unit x, its first unit, and the units of a head of it
+    long long base, per_head;
 };
 
 // Where unit x of the line lies: the CTA sums every sequence's units, a run
@@ -90,13 +91,17 @@ struct Line {
 template <class F>
 __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x_of) {
     __shared__ long long s_sum[32];
-    __shared__ long long s_base;
+    __shared__ long long s_base, s_head;
     __shared__ int s_seq;
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (p.n_seqs + nt - 1) / nt;
     const int a = (int)min((long long)p.n_seqs, (long long)threadIdx.x * per), b = min(p.n_seqs, a + per);
-    long long mine = 0;
-    for (int i = 0; i < per; ++i) mine += lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hn;
+    long long mine = 0, first = 0;
+    for (int i = 0; i < per; ++i) {
+        const long long u = lane_units(p, pl, a + i < b ? a + i : p.n_seqs);
+        if (i == 0) first = u;
+        mine += u * p.Hn;
+    }
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -104,7 +109,7 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
         if (lane >= o) inc += y;
     }
     if (lane == 31) s_sum[warp] = inc;
-    if (threadIdx.x == 0) { s_seq = p.n_seqs; s_base = 0; }
+    if (threadIdx.x == 0) { s_seq = p.n_seqs; s_base = s_head = 0; }
     __syncthreads();
     Line l;
     l.total = 0;
@@ -117,17 +122,19 @@ __device__ Line find_unit(const AttendParams& p, const Plan& pl, int n_ctas, F x
     const long long x = x_of(l);
     if (__any_sync(0xffffffffu, x >= before && x < before + mine)) {
         for (int i = 0; i < per; ++i) {
-            const long long u = lane_units(p, pl, a + i < b ? a + i : p.n_seqs) * p.Hn;
-            if (x >= before && x < before + u) {
+            const long long u = i == 0 ? first : lane_units(p, pl, a + i < b ? a + i : p.n_seqs);
+            if (x >= before && x < before + u * p.Hn) {
                 s_seq = a + i;
                 s_base = before;
+                s_head = u;
             }
-            before += u;
+            before += u * p.Hn;
         }
     }
     __syncthreads();
     l.seq = s_seq;
     l.base = s_base;
+    l.per_head = s_head;
     return l;
 }
 
@@ -139,16 +146,14 @@ struct Item {
     long long begin;          // first unit
 
     __device__ void load(const AttendParams& p, const Plan& pl) { tile = tile_of(p, pl, rows, rt); }
-    // The item that holds unit x >= base of sequence seq (all lanes of a warp
-    // together).
-    __device__ bool seek(const AttendParams& p, const Plan& pl, int seq, long long base, long long x) {
-        s = seq;
+    // The item of the line that holds unit x (all lanes of a warp together).
+    __device__ bool seek(const AttendParams& p, const Plan& pl, const Line& l, long long x) {
+        s = l.seq;
         if (s >= p.n_seqs) return false;
         rows = seq_rows(p, s);
-        const long long per_head = head_units(p, pl, rows);
-        const int h = (int)((x - base) / per_head);
+        const int h = (int)((x - l.base) / l.per_head);
         head = p.h0 + h;
-        begin = base + h * per_head;
+        begin = l.base + h * l.per_head;
         const int n = n_row_tiles(p, pl, rows), lane = threadIdx.x & 31;
         for (rt = 0;; rt += 32) {
             const long long u = rt + lane < n ? tile_of(p, pl, rows, rt + lane).units : 0;
@@ -240,7 +245,7 @@ __host__ __device__ constexpr int many_rows(int D) { return D == 256 ? 128 : 256
 
 // Images of key tiles: tokens of a tile, bytes (keys and values in fp16, three
 // floats a token), and what a workspace holds of them: half of L2.
-__host__ __device__ constexpr int image_tokens(int D) { return D == 256 ? 64 : 128; }
+__host__ __device__ constexpr int image_tokens(int) { return 64; }
 __host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12); }
 constexpr size_t kImageBytes = 64u << 20;
 constexpr int kImageRowTiles = 4;       // images are made for more row tiles than this

@@ -8,7 +8,7 @@
 //
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
-// 128 (64) tokens:
+// 64 tokens:
 //   softmax      four warps per query tile: a thread owns a row; S comes from
 //                tensor memory in pieces of 32 columns, P goes back over it as
 //                the A operand.
@@ -18,8 +18,7 @@
 //                layout read as MN-major is the value operand, so neither is
 //                transposed.
 //   issue        one thread: S = Q K^T and O += P V
-// With two query tiles the softmax of one runs beside the products of the
-// other; with one, two score buffers let the next S run ahead.  The row's
+// Two score buffers per query tile let the next S run ahead of the softmax.  The row's
 // reference m is raised as in the kernel for few rows, and to a whole number,
 // so that what it rescales (O, and the P of the tile's earlier pieces)
 // changes by a power of two: the scores are gone
@@ -40,13 +39,15 @@ namespace {
 using namespace sm100;
 using namespace attend;
 
+constexpr int kExtra = 4;                        // loading the queries and writing the sums, in key tiles
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 constexpr uint64_t kDrainLimit = 20000000ull;    // and per wait for a copy in flight after one gave up
 
 template <int D, bool IMG>
 struct Many {
     static constexpr int NQ = D == 256 ? 1 : 2;       // query tiles of 128 rows
-    static constexpr int TK = D == 256 ? 64 : 128;    // tokens of a key tile
+    static constexpr int TK = 64;                     // tokens of a key tile
+    static constexpr int NST = D == 256 ? 2 : 4;      // stages of keys, and of values
     static constexpr int kRows = NQ * 128;
     static constexpr int kKeyWarp = 4 * NQ, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
                          kMmaWarp = kValueWarp + (IMG ? 0 : 4);
@@ -55,8 +56,8 @@ struct Many {
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
     static constexpr size_t kImage = 2 * kOpBytes + kScaleBytes;   // keys, values, scales of a tile
-    static constexpr size_t kSmem = 1024 + NQ * kQBytes + 4 * kOpBytes + 2 * kScaleBytes + 256;
-    static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 (b * TK), sums from 256 (q * D)
+    static constexpr size_t kSmem = 1024 + NQ * kQBytes + NST * (2 * kOpBytes + kScaleBytes) + 512;
+    static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 ((2 q + b) * TK), sums from 256 (q * D)
 };
 
 // MN-major operand: 64 elements of N (128 bytes, swizzled) by 8 of K per
@@ -159,8 +160,9 @@ struct Walk {
     __device__ void open(const AttendParams& p, const Plan& pl) {
         u0 = (int)(x - it.begin);
         u1 = (int)min((long long)it.tile.units, x_end - it.begin);
-        t0 = it.tile.step0 + u0;
-        t1 = min(it.tile.step1, it.tile.step0 + u1);
+        t0 = it.tile.step0 + max(0, u0 - pl.extra);
+        t1 = it.tile.step0 + max(0, u1 - pl.extra);
+        t1 = min(t1, it.tile.step1);
         n_rows = min(pl.rows, it.rows.n * p.G - it.rt * pl.rows);
     }
     __device__ bool next(const AttendParams& p, const Plan& pl) {
@@ -174,39 +176,43 @@ struct Walk {
 template <int D, int FMT, bool IMG>
 __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(AttendParams p, Plan pl) {
     using C = Many<D, IMG>;
-    constexpr int NQ = C::NQ, TK = C::TK;
+    constexpr int NQ = C::NQ, TK = C::TK, NST = C::NST;
+    constexpr int kStLog2 = NST == 2 ? 1 : 2;
+    constexpr int PW = IMG ? 64 : 32;            // columns of a softmax piece (registers: 168 a thread, or 96 to 128)
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
     char* sq = smem;
     char* sk = sq + NQ * C::kQBytes;
-    char* sv = sk + 2 * C::kOpBytes;
-    float* ssc = reinterpret_cast<float*>(sv + 2 * C::kOpBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ssc) + 2 * C::kScaleBytes);
-    uint64_t* k_full = bars;         // [2] keys and scales of a stage written (4 warps)
-    uint64_t* v_full = bars + 2;     // [2]
-    uint64_t* k_empty = bars + 4;    // [2] read by the tensor core (commit)
-    uint64_t* v_empty = bars + 6;    // [2]
-    uint64_t* s_full = bars + 8;     // [2] scores of a buffer done (commit)
-    uint64_t* p_full = bars + 10;    // [2] probabilities written (4 warps)
-    uint64_t* o_done = bars + 12;    // [2] sums of a query tile updated (commit)
-    uint64_t* q_full = bars + 14;    // [2] query tile written (4 warps)
-    uint64_t* sc_free = bars + 16;   // [2] scales of a stage read (4 NQ warps)
-    uint64_t* final_bar = bars + 18;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
+    char* sv = sk + NST * C::kOpBytes;
+    float* ssc = reinterpret_cast<float*>(sv + NST * C::kOpBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ssc) + NST * C::kScaleBytes);
+    uint64_t* k_full = bars;         // [NST] keys and scales of a stage written
+    uint64_t* v_full = bars + 4;     // [NST]
+    uint64_t* k_empty = bars + 8;    // [NST] read by the tensor core (commit)
+    uint64_t* v_empty = bars + 12;   // [NST]
+    uint64_t* sc_free = bars + 16;   // [NST] scales of a stage read (4 NQ warps)
+    uint64_t* s_full = bars + 20;    // [2 q + b] scores of a buffer done (commit)
+    uint64_t* p_full = bars + 24;    // [2 q + b] probabilities written (4 warps)
+    uint64_t* o_done = bars + 28;    // [q] sums of a query tile updated (commit)
+    uint64_t* q_full = bars + 30;    // [q] query tile written (4 warps)
+    uint64_t* final_bar = bars + 32;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&k_full[i], IMG ? 1 : 4);
             mbar_init(&v_full[i], IMG ? 1 : 4);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
+            mbar_init(&sc_free[i], 4 * NQ);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&o_done[i], 1);
             mbar_init(&q_full[i], 4);
-            mbar_init(&sc_free[i], 4 * NQ);
         }
         mbar_init(final_bar, 1);
         *abort_flag = 0;
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     w.x_end = min(line.total, x_begin + line.chunk);
     bool more = w.x < w.x_end;
     if (more) {
-        w.it.seek(p, pl, line.seq, line.base, w.x);
+        w.it.seek(p, pl, line, w.x);
         w.open(p, pl);
     }
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1, abort_flag, kWaitLimit); };
@@ -253,42 +259,41 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             float m = -INFINITY, l = 0.f;
             f2 m2 = 0ull;                // -m twice; 0 while m is -infinity
             if (active && w.t0 < w.t1) {
-                // this row as fp16, scaled by a power of two
-                float a = 0.f, scale = 0.f;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + (size_t)(w.it.rows.q0 + rowid / p.G) * p.q_stride + (size_t)(w.it.head * p.G + rowid % p.G) * D);
-                char* dst = sq + q * C::kQBytes + row * 128;
-                uint32_t mb = 0;
-                if (live)
+                // the warp's 32 rows as fp16, each scaled by a power of two (past
+                // the last row: a copy of it, so that no load is conditional)
+                constexpr int LPR = D / 8, RPL = 32 / LPR;       // lanes of a row, rows of a pass
+                float scale = 0.f;
 #pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint4 v = __ldg(src + i);
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                for (int i = 0; i < LPR; ++i) {
+                    const int rw = i * RPL + lane / LPR, ch = lane % LPR;
+                    const int id = w.it.rt * C::kRows + min(q * 128 + 32 * (warp & 3) + rw, w.n_rows - 1);
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                                              p.q + (size_t)(w.it.rows.q0 + id / p.G) * p.q_stride +
+                                              (size_t)(w.it.head * p.G + id % p.G) * D) + ch);
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t mb = 0;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) mb = max(mb, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
-                    }
-                a = bf16_bits_to_f32(mb);
-                const bool bad = mb >= 0x7f80u;
-                int e = (int)(__float_as_uint(a) >> 23) - 127;
-                e = min(max(e, -100), 126);
-                const float down = bad ? 0.f : __uint_as_float((uint32_t)(127 - e) << 23);
-                scale = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    uint4 o = make_uint4(0, 0, 0, 0);
-                    if (live && !bad) {
-                        const uint4 v = __ldg(src + i);
-                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                        uint32_t h[4];
+                    for (int j = 0; j < 4; ++j) mb = max(mb, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f = bf16x2_to_f32x2(u[j]);
-                            const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
-                            h[j] = *reinterpret_cast<const uint32_t*>(&hh);
-                        }
-                        o = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int o = LPR / 2; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+                    const bool bad = mb >= 0x7f80u;
+                    const int e = min(max((int)(mb >> 7) - 127, -100), 126);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    const float up = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int j = 0; j < RPL; ++j) {
+                        const float y = __shfl_sync(0xffffffffu, up, j * LPR);
+                        if (lane == i * RPL + j) scale = y;
                     }
-                    *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (row & 7)) << 4)) = o;
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = bf16x2_to_f32x2(u[j]);
+                        const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
+                        h[j] = bad ? 0u : *reinterpret_cast<const uint32_t*>(&hh);
+                    }
+                    *reinterpret_cast<uint4*>(sq + q * C::kQBytes + (32 * (warp & 3) + rw) * 128 + (ch >> 3) * (128 * 128) +
+                                              (((ch & 7) ^ (rw & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -296,9 +301,8 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                 const f2 scale2 = pack2(scale, scale);
 
                 for (int t = w.t0; t < w.t1; ++t, ++n, ++cnt) {
-                    const int st = n & 1, b = NQ == 2 ? q : st;
-                    const uint32_t sph = NQ == 2 ? cnt : n >> 1;
-                    dead = !wait(&k_full[st], n >> 1) || !wait(&s_full[b], sph);
+                    const int st = n & (NST - 1), b = 2 * q + (cnt & 1);
+                    dead = !wait(&k_full[st], n >> kStLog2) || !wait(&s_full[b], cnt >> 1);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     tc_fence_after();
@@ -312,13 +316,15 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     const bool mask = __any_sync(0xffffffffu, hi < TK || lo > 0);
                     f2 l2 = pack2(0.f, 0.f);
 #pragma unroll 1
-                    for (int c = 0; c < TK / 32; ++c, ks += 8, hi -= 32, lo -= 32) {
-                        uint32_t x[32];
-                        tmem_ld_32x32b_x32(tS + 32 * c, x);
+                    for (int c = 0; c < TK / PW; ++c, ks += PW / 4, hi -= PW, lo -= PW) {
+                        uint32_t x[PW];
+#pragma unroll
+                        for (int i = 0; i < PW / 32; ++i)
+                            tmem_ld_32x32b_x32(tS + PW * c + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * i));
                         tmem_ld_wait();
                         float top = -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < PW / 4; ++i) {
                             const float4 k4 = ks[i], b4 = ks[TK / 4 + i];
                             uint32_t* y = x + 4 * i;
                             const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y)));
@@ -330,11 +336,11 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         }
                         if (mask) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < PW; ++i)
                                 if (i < lo || i >= hi) x[i] = 0xff800000u;
                         }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                        for (int i = 0; i < PW; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
                         if (__any_sync(0xffffffffu, top > m + kMaxP)) {
                             const float mn = fmaxf(m, ceilf(top) - kRaiseP);
                             const float f = m == mn ? 1.f : ex2(m - mn);
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                             }
                             const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
-                            for (int d = 0; d < c; ++d) {
+                            for (int d = 0; d < c * (PW / 32); ++d) {
                                 uint32_t o[16];
                                 tmem_ld_32x32b_x16(tS + 16 * d, o);
                                 tmem_ld_wait();
@@ -372,21 +378,24 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                                 tmem_st_32x32b_x16(tS + 16 * d, o);
                             }
                         }
-                        uint32_t ph[16];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 i4 = ks[TK / 2 + i];
-                            const uint32_t* y = x + 4 * i;
-                            const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2));
-                            const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2));
-                            const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
-                            l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
-                            l2 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2);
-                            const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-                            ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
-                            ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                        for (int g = 0; g < PW / 32; ++g) {
+                            uint32_t ph[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 i4 = ks[TK / 2 + 8 * g + i];
+                                const uint32_t* y = x + 32 * g + 4 * i;
+                                const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2));
+                                const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2));
+                                const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                                l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
+                                l2 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2);
+                                const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+                                ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+                                ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                            }
+                            tmem_st_32x32b_x16(tS + 16 * (c * (PW / 32) + g), ph);
                         }
-                        tmem_st_32x32b_x16(tS + 16 * c, ph);
                     }
                     if (dead) break;
                     const float2 ls = unpack2(l2);
@@ -407,10 +416,10 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                 __syncwarp();
             } else {
                 for (int t = w.t0; t < w.t1; ++t, ++n) {      // a query tile without rows only lets the scales go
-                    dead = !wait(&k_full[n & 1], n >> 1);
+                    dead = !wait(&k_full[n & (NST - 1)], n >> kStLog2);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
-                    if (lane == 0) mbar_arrive(&sc_free[n & 1]);
+                    if (lane == 0) mbar_arrive(&sc_free[n & (NST - 1)]);
                 }
                 if (dead) break;
             }
@@ -436,16 +445,30 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                             d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
                     } else if (live) {
-                        uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < 4; ++i) {            // through the query tile's place, for whole-row stores
+                            const int ch = 4 * c + i;
                             uint32_t h[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 h[j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j]) * inv) |
                                        (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j + 1]) * inv) << 16;
-                            d[i] = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4*>(sq + q * C::kQBytes + row * 128 + (ch >> 3) * (128 * 128) +
+                                                      (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
+                    }
+                    __syncwarp();
+                }
+                const int last = w.n_rows - 1 - q * 128 - 32 * (warp & 3);       // the warp's last row
+                if (!cut && last >= 0) {
+                    constexpr int LPR = D / 8, RPL = 32 / LPR;
+#pragma unroll 4
+                    for (int i = 0; i < LPR; ++i) {
+                        const int rw = min(i * RPL + lane / LPR, last), ch = lane % LPR;   // (the last row: repeated)
+                        const int id = w.it.rt * C::kRows + q * 128 + 32 * (warp & 3) + rw;
+                        const size_t at = (size_t)(w.it.rows.q0 + id / p.G) * p.Hq + w.it.head * p.G + id % p.G;
+                        *(reinterpret_cast<uint4*>(p.out + at * D) + ch) = *reinterpret_cast<const uint4*>(
+                            sq + q * C::kQBytes + (32 * (warp & 3) + rw) * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rw & 7)) << 4));
                     }
                     __syncwarp();
                 }
@@ -473,8 +496,8 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                 const char* img = p.img + ((size_t)w.it.s * p.Hn + (w.it.head - p.h0)) * p.img_tiles * C::kImage;
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const char* src = img + (size_t)t * C::kImage;
-                    const int st = n & 1;
-                    const uint32_t ph = (n >> 1) ^ 1;
+                    const int st = n & (NST - 1);
+                    const uint32_t ph = (n >> kStLog2) ^ 1;
                     dead = !wait(&sc_free[st], ph) || !wait(&k_empty[st], ph);
                     if (dead) break;
                     mbar_arrive_expect_tx(&k_full[st], (uint32_t)(C::kOpBytes + C::kScaleBytes));
@@ -491,11 +514,11 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             }
             // the copies in flight end before the CTA does, after an abort too
             volatile int no_abort = 0;
-            for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) {
-                mbar_wait(&k_full[i & 1], (i >> 1) & 1, &no_abort, kDrainLimit);
-                mbar_wait(&v_full[i & 1], (i >> 1) & 1, &no_abort, kDrainLimit);
+            for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i) {
+                mbar_wait(&k_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
+                mbar_wait(&v_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
             }
-            if (half) mbar_wait(&k_full[n & 1], (n >> 1) & 1, &no_abort, kDrainLimit);
+            if (half) mbar_wait(&k_full[n & (NST - 1)], (n >> kStLog2) & 1, &no_abort, kDrainLimit);
         }
         __syncwarp();
     } else if (!IMG && warp < C::kMmaWarp) {
@@ -576,8 +599,8 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             ++t;
             settle();
             locate();
-            const int st = n & 1;
-            const uint32_t ph = (n >> 1) ^ 1;
+            const int st = n & (NST - 1);
+            const uint32_t ph = (n >> kStLog2) ^ 1;
             bool dead = !wait(&empty[st], ph) || (keys && !wait(&sc_free[st], ph));
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
@@ -613,65 +636,53 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             auto scores = [&](int q, int b, int st) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_f16(tmem + b * TK, sdesc_k128(q_base + q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32),
+                    umma_f16(tmem + (2 * q + b) * TK, sdesc_k128(q_base + q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32),
                              sdesc_k128(k_base + st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32), idesc_s, k > 0);
-                umma_commit(&s_full[b]);
+                umma_commit(&s_full[2 * q + b]);
             };
             auto sums = [&](int q, int b, int st, bool first) {
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k)
-                    umma_f16_ts(tmem + C::kColO + q * D, tmem + b * TK + 8 * k,
+                    umma_f16_ts(tmem + C::kColO + q * D, tmem + (2 * q + b) * TK + 8 * k,
                                 sdesc_mn128(v_base + st * C::kOpBytes + k * 2048, TK * 128), idesc_o, !first || k > 0);
                 umma_commit(&o_done[q]);
             };
-            uint32_t n = 0, cnt[2] = {0, 0}, qc[2] = {0, 0};
+            uint32_t n = 0, ns[2] = {0, 0}, np[2] = {0, 0}, qc[2] = {0, 0};   // tiles, and per query tile
             bool ok = true, issued = false;
             while (more && ok) {
                 const int J = w.t1 - w.t0;
                 const int nq = NQ == 2 && w.n_rows > 128 ? 2 : 1;
                 if (J > 0) {
                     for (int q = 0; q < nq && ok; ++q) ok = wait(&q_full[q], qc[q]++);
-                    if (ok) ok = wait(&k_full[n & 1], n >> 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issued = true;
-                    for (int q = 0; q < nq; ++q) scores(q, NQ == 2 ? q : n & 1, n & 1);
-                    umma_commit(&k_empty[n & 1]);
-                    for (int j = 0; j < J && ok; ++j, ++n) {
-                        const int st = n & 1, st1 = st ^ 1;
-                        const bool ahead = j + 1 < J;
-                        if (NQ == 1) {
-                            if (ahead) {
-                                ok = wait(&k_full[st1], (n + 1) >> 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                                scores(0, st1, st1);
-                                umma_commit(&k_empty[st1]);
-                            }
-                            ok = wait(&v_full[st], n >> 1) && wait(&p_full[st], n >> 1);
+                    for (int j = -1; j < J && ok; ++j) {
+                        // the scores of the next tile first: the softmax finds them when it is done with this one's
+                        if (j + 1 < J) {
+                            const uint32_t m = n + (j >= 0 ? 1 : 0);
+                            const int st = m & (NST - 1);
+                            ok = wait(&k_full[st], m >> kStLog2);
                             if (!ok) break;
                             tc_fence_after();
-                            sums(0, st, st, j == 0);
-                        } else {
-                            ok = wait(&v_full[st], n >> 1);
-                            for (int q = 0; q < nq && ok; ++q) {
-                                ok = wait(&p_full[q], cnt[q]++);
+                            issued = true;
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                if (q < nq) scores(q, ns[q]++ & 1, st);
+                            umma_commit(&k_empty[st]);
+                        }
+                        if (j < 0) continue;
+                        const int st = n & (NST - 1);
+                        ok = wait(&v_full[st], n >> kStLog2);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            if (q < nq && ok) {
+                                const int b = np[q] & 1;
+                                ok = wait(&p_full[2 * q + b], np[q]++ >> 1);
                                 if (!ok) break;
                                 tc_fence_after();
-                                sums(q, q, st, j == 0);
-                                if (ahead) {
-                                    if (q == 0) {
-                                        ok = wait(&k_full[st1], (n + 1) >> 1);
-                                        if (!ok) break;
-                                        tc_fence_after();
-                                    }
-                                    scores(q, q, st1);
-                                }
+                                sums(q, b, st, j == 0);
                             }
-                            if (!ok) break;
-                            if (ahead) umma_commit(&k_empty[st1]);
-                        }
+                        if (!ok) break;
                         umma_commit(&v_empty[st]);
+                        ++n;
                     }
                 }
                 if (ok) more = w.next(p, pl);
@@ -760,7 +771,7 @@ template <int D, int FMT, bool IMG>
 cudaError_t launch(const AttendParams& p, cudaStream_t st) {
     using C = Many<D, IMG>;
     static_assert(C::kRows == many_rows(D) && C::kImage == image_bytes(D) && C::TK == image_tokens(D), "sizes");
-    const Plan pl{C::kRows, D == 256 ? 6 : 7, 1};
+    const Plan pl{C::kRows, 6, 1, kExtra};
     cudaError_t e = allow_smem<k_attend_many<D, FMT, IMG>>(C::kSmem);
     if (e != cudaSuccess) return e;
     k_attend_many<D, FMT, IMG><<<kSms, C::kThreads, C::kSmem, st>>>(p, pl);

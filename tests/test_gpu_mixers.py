@@ -170,6 +170,36 @@ def test_attend_chunks(fmt, Hq, Hk, D, page, ns, kv):
     check_attend(fmt, Hq, Hk, D, page, ns, kv, seed=Hq + D, pad=2)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 70), (False, 0)])
+@pytest.mark.parametrize("Hq,Hk,D,page,ns,kv", [
+    (8, 1, 64, 16, [140, 1], [700, 70]),
+    (10, 2, 128, 64, [210, 0, 30], [210, 9, 400]),
+    (5, 1, 256, 128, [110, 3], [300, 65]),
+])
+def test_attend_many_row_tiles(fmt, causal, window, Hq, Hk, D, page, ns, kv):
+    """More than four row tiles per key head."""
+    check_attend(fmt, Hq, Hk, D, page, ns, kv, causal=causal, window=window, seed=Hq + D, pad=1)
+
+
+@pytest.mark.parametrize("pages,kv_heads", [(1200, 3), (2000, 3), (3000, 2), (6000, 2)])
+def test_attend_with_room_for_long_contexts(pages, kv_heads):
+    """Page tables so wide that a launch takes several sequences, one, some heads of one, or none as images."""
+    D, page, ns, kv = 256, 16, [90, 91, 2], [100, 150, 40]
+    cache = R.Cache("int8", kv_heads, D, page, kv, seed=pages)
+    cache.table = torch.cat([cache.table, torch.full((3, pages - cache.table.shape[1]), -7, dtype=torch.int32)], 1)
+    pk = paged(cache, 6 * kv_heads, kv_heads, D)
+    ws = pk.workspace()
+    q = torch.randn(sum(ns), 6 * kv_heads, D, generator=torch.Generator().manual_seed(1)).bfloat16()
+    out = pk.attend(q.to(DEV), batch_of(pk, cache, ns), ws)
+    assert B.lmoe_last_device_status(ws) == B.LMOE_OK
+    t0 = 0
+    for s, n in enumerate(ns):
+        want, _, tol, _ = R.attend(q[t0:t0 + n], cache.rows("k", s), cache.rows("v", s), kv[s] - n, D ** -0.5, True, 0)
+        R.assert_within(out[t0:t0 + n], want, tol, f"out of sequence {s}")
+        t0 += n
+
+
 @pytest.mark.parametrize("window", [1, 16, 100])
 @pytest.mark.parametrize("Hq,Hk,D,ns,kv", [(4, 2, 128, [1, 3], [500, 40]), (4, 4, 64, [200, 5], [301, 5]), (4, 2, 256, [40], [150])])
 def test_attend_window(window, Hq, Hk, D, ns, kv):
