@@ -9,9 +9,11 @@
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
 // 64 tokens:
-//   softmax      four warps per query tile: a thread owns a row; S comes from
-//                tensor memory in pieces of 32 columns, P goes back over it as
-//                the A operand.
+//   softmax      eight warps: a thread has a row of each query tile and half of
+//                the columns; S comes from tensor memory, P goes back over it
+//                as the A operand.  (Two rows a thread share the loads of the
+//                tokens' constants: shared memory, which feeds the tensor core
+//                as well, is what runs out first.)
 //   keys, values four warps each read the codes of a tile (registers, one tile
 //                ahead) and write them as fp16 operands with the 128-byte
 //                swizzle; a key row is K-major as it is stored, and the same
@@ -49,14 +51,14 @@ struct Many {
     static constexpr int TK = 64;                     // tokens of a key tile
     static constexpr int NST = D == 256 ? 2 : 4;      // stages of keys, and of values
     static constexpr int kRows = NQ * 128;
-    static constexpr int kKeyWarp = 4 * NQ, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
+    static constexpr int kKeyWarp = 8, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
                          kMmaWarp = kValueWarp + (IMG ? 0 : 4);
     static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
     static constexpr size_t kImage = 2 * kOpBytes + kScaleBytes;   // keys, values, scales of a tile
-    static constexpr size_t kSmem = 1024 + NQ * kQBytes + NST * (2 * kOpBytes + kScaleBytes) + 512;
+    static constexpr size_t kSmem = 1024 + NQ * kQBytes + 2 * NST * kOpBytes + 4 * kScaleBytes + 512;
     static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 ((2 q + b) * TK), sums from 256 (q * D)
 };
 
@@ -74,14 +76,32 @@ __device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t lbo) {
 
 constexpr uint32_t kTransposeB = 1u << 16;   // instruction descriptor: B is MN-major
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Products and commits are issued by a whole warp, converged, one elected lane
+// of it: 48 cycles for M 128, N 64, K 16 (shared memory's pace), where a
+// single lane in a divergent branch needs 60 to 100 to get one out.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 
@@ -92,6 +112,17 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -178,25 +209,30 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     using C = Many<D, IMG>;
     constexpr int NQ = C::NQ, TK = C::TK, NST = C::NST;
     constexpr int kStLog2 = NST == 2 ? 1 : 2;
-    constexpr int PW = IMG ? 64 : 32;            // columns of a softmax piece (registers: 168 a thread, or 96 to 128)
+    constexpr int CW = TK / 2;                   // columns of a softmax warp
+    constexpr int PW = IMG ? CW : 16;            // columns of a piece (registers: 168 a thread, or 96)
+    __shared__ float s_row[2][2][NQ][128];       // exchange between the two warps of a row
+    __shared__ float s_scale[NQ][128];
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
     char* sq = smem;
     char* sk = sq + NQ * C::kQBytes;
     char* sv = sk + NST * C::kOpBytes;
     float* ssc = reinterpret_cast<float*>(sv + NST * C::kOpBytes);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ssc) + NST * C::kScaleBytes);
-    uint64_t* k_full = bars;         // [NST] keys and scales of a stage written
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(ssc) + 4 * C::kScaleBytes);
+    uint64_t* k_full = bars;         // [NST] keys of a stage written
     uint64_t* v_full = bars + 4;     // [NST]
     uint64_t* k_empty = bars + 8;    // [NST] read by the tensor core (commit)
     uint64_t* v_empty = bars + 12;   // [NST]
-    uint64_t* sc_free = bars + 16;   // [NST] scales of a stage read (4 NQ warps)
-    uint64_t* s_full = bars + 20;    // [2 q + b] scores of a buffer done (commit)
-    uint64_t* p_full = bars + 24;    // [2 q + b] probabilities written (4 warps)
-    uint64_t* o_done = bars + 28;    // [q] sums of a query tile updated (commit)
-    uint64_t* q_full = bars + 30;    // [q] query tile written (4 warps)
-    uint64_t* final_bar = bars + 32;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
+    uint64_t* sc_free = bars + 16;   // [4] scales of a stage read (8 warps)
+    uint64_t* s_full = bars + 20;    // [b] scores of a buffer done (commit)
+    uint64_t* p_full = bars + 22;    // [b] probabilities written (8 warps)
+    uint64_t* o_done = bars + 24;    // sums updated (commit)
+    uint64_t* q_full = bars + 25;    // query tiles written (8 warps)
+    uint64_t* sc_full = bars + 32;   // [4] scales of a stage written
+    uint64_t* pair = bars + 36;      // [4] the two warps of a row
+    uint64_t* final_bar = bars + 40;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 41);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -206,14 +242,16 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             mbar_init(&v_full[i], IMG ? 1 : 4);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
-            mbar_init(&sc_free[i], 4 * NQ);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&sc_full[i], IMG ? 1 : 4);
+            mbar_init(&sc_free[i], 8);
+            mbar_init(&pair[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&o_done[i], 1);
-            mbar_init(&q_full[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 8);
         }
+        mbar_init(o_done, 1);
+        mbar_init(q_full, 8);
         mbar_init(final_bar, 1);
         *abort_flag = 0;
         p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -242,31 +280,51 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     }
     auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity & 1, abort_flag, kWaitLimit); };
 
-    if (warp < 4 * NQ) {
+    if (warp < 8) {
         // ------------------------------------------------------ softmax
-        const int q = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tO = tmem + lanes + C::kColO + q * D;
-        uint32_t n = 0, cnt = 0;     // key tiles of the CTA, and those of this query tile
+        const int half = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+        const uint32_t tO = tmem + lanes + C::kColO;
+        uint32_t n = 0;              // key tiles of the CTA
+        uint32_t met = 0;            // meetings of the two warps of a row
         bool dead = false;
+        auto meet = [&]() {          // false: given up
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pair[quad]);
+            const bool ok = wait(&pair[quad], met++);
+            return !__any_sync(0xffffffffu, !ok);
+        };
+        // 16 bytes of a row of a query tile's place (fp16 queries, later bf16 sums)
+        auto place = [&](int q, int rw, int ch) {
+            return reinterpret_cast<uint4*>(sq + q * C::kQBytes + (32 * quad + rw) * 128 + (ch >> 3) * (128 * 128) +
+                                            (((ch & 7) ^ (rw & 7)) << 4));
+        };
         while (more && !dead) {
-            const int r = q * 128 + row;
-            const bool live = r < w.n_rows;
-            const bool active = q * 128 < w.n_rows;      // the query tile has rows
-            const int rowid = w.it.rt * C::kRows + r;
-            const size_t orow = (size_t)(w.it.rows.q0 + rowid / p.G) * p.Hq + w.it.head * p.G + rowid % p.G;
-            const int pos = w.it.rows.kv - w.it.rows.n + rowid / p.G;
-            float m = -INFINITY, l = 0.f;
-            f2 m2 = 0ull;                // -m twice; 0 while m is -infinity
-            if (active && w.t0 < w.t1) {
-                // the warp's 32 rows as fp16, each scaled by a power of two (past
-                // the last row: a copy of it, so that no load is conditional)
+            const int nq = w.n_rows > 128 ? NQ : 1;      // query tiles with rows
+            const int row0 = w.it.rt * C::kRows;
+            float m[NQ], l[NQ];
+            f2 m2[NQ];               // -m twice; 0 while m is -infinity
+            int pos[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                m[q] = -INFINITY;
+                l[q] = 0.f;
+                m2[q] = 0ull;
+                pos[q] = w.it.rows.kv - w.it.rows.n + (row0 + q * 128 + row) / p.G;
+            }
+            const bool some = w.t0 < w.t1;
+            if (some) {
+                dead = !meet();      // both have stored the last item's sums from the tiles' places
+                if (dead) break;
+                // rows as fp16, each scaled by a power of two (past the last
+                // row: a copy of it, so that no load is conditional); the two
+                // warps take a tile each, or every other pass
                 constexpr int LPR = D / 8, RPL = 32 / LPR;       // lanes of a row, rows of a pass
-                float scale = 0.f;
+                const int qt = NQ == 2 ? half : 0;
 #pragma unroll 4
-                for (int i = 0; i < LPR; ++i) {
+                for (int i = NQ == 2 ? 0 : half; i < LPR; i += 3 - NQ) {
                     const int rw = i * RPL + lane / LPR, ch = lane % LPR;
-                    const int id = w.it.rt * C::kRows + min(q * 128 + 32 * (warp & 3) + rw, w.n_rows - 1);
+                    const int id = row0 + min(qt * 128 + 32 * quad + rw, w.n_rows - 1);
                     const uint4 v = __ldg(reinterpret_cast<const uint4*>(
                                               p.q + (size_t)(w.it.rows.q0 + id / p.G) * p.q_stride +
                                               (size_t)(w.it.head * p.G + id % p.G) * D) + ch);
@@ -279,12 +337,9 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     const bool bad = mb >= 0x7f80u;
                     const int e = min(max((int)(mb >> 7) - 127, -100), 126);
                     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    const float up = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                    for (int j = 0; j < RPL; ++j) {
-                        const float y = __shfl_sync(0xffffffffu, up, j * LPR);
-                        if (lane == i * RPL + j) scale = y;
-                    }
+                    if (ch == 0)
+                        s_scale[qt][32 * quad + rw] =
+                            bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
                     uint32_t h[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -292,114 +347,159 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
                         h[j] = bad ? 0u : *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    *reinterpret_cast<uint4*>(sq + q * C::kQBytes + (32 * (warp & 3) + rw) * 128 + (ch >> 3) * (128 * 128) +
-                                              (((ch & 7) ^ (rw & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *place(qt, rw, ch) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[q]);
-                const f2 scale2 = pack2(scale, scale);
+                if (lane == 0) mbar_arrive(q_full);
+                dead = !meet();
+                if (dead) break;
+                f2 scale2[NQ];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) scale2[q] = pack2(s_scale[q][row], s_scale[q][row]);
 
-                for (int t = w.t0; t < w.t1; ++t, ++n, ++cnt) {
-                    const int st = n & (NST - 1), b = 2 * q + (cnt & 1);
-                    dead = !wait(&k_full[st], n >> kStLog2) || !wait(&s_full[b], cnt >> 1);
+                for (int t = w.t0; t < w.t1; ++t, ++n) {
+                    const int st = n & 3, b = n & 1;
+                    dead = !wait(&sc_full[st], n >> 2) || !wait(&s_full[b], n >> 1);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t tS = tmem + lanes + b * TK;
-                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
-                    const int tok0 = t * TK;
-                    // keys this row sees: columns lo .. hi - 1
-                    int hi = p.causal ? pos + 1 - tok0 : TK;
-                    int lo = p.window ? pos + 1 - p.window - tok0 : 0;
-                    const bool mask = __any_sync(0xffffffffu, hi < TK || lo > 0);
-                    f2 l2 = pack2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < TK / PW; ++c, ks += PW / 4, hi -= PW, lo -= PW) {
-                        uint32_t x[PW];
+                    const uint32_t tS = tmem + lanes + b * TK;       // (query tile q: 2 q TK on)
+                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4) + half * CW);
+                    const int tok0 = t * TK + half * CW;
+                    // keys a row sees: columns lo .. hi - 1
+                    int hi[NQ], lo[NQ];
+                    bool edge = false;
 #pragma unroll
-                        for (int i = 0; i < PW / 32; ++i)
-                            tmem_ld_32x32b_x32(tS + PW * c + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * i));
+                    for (int q = 0; q < NQ; ++q) {
+                        hi[q] = p.causal ? pos[q] + 1 - tok0 : CW;
+                        lo[q] = p.window ? pos[q] + 1 - p.window - tok0 : 0;
+                        edge |= hi[q] < CW || lo[q] > 0;
+                    }
+                    const bool mask = __any_sync(0xffffffffu, edge);
+                    f2 l2[NQ];
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) l2[q] = pack2(0.f, 0.f);
+#pragma unroll 1
+                    for (int c = 0; c < CW / PW; ++c, ks += PW / 4) {
+                        uint32_t x[NQ][PW];
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                            for (int i = 0; i < PW / 16; ++i)
+                                tmem_ld_32x32b_x16(tS + 2 * q * TK + half * CW + PW * c + 16 * i,
+                                                   *reinterpret_cast<uint32_t(*)[16]>(x[q] + 16 * i));
                         tmem_ld_wait();
-                        float top = -INFINITY;
+                        float top[NQ];
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) top[q] = -INFINITY;
+                        // the tokens' constants come from shared memory, whose
+                        // bandwidth the tensor core's operands need most of:
+                        // one load serves both query tiles
 #pragma unroll
                         for (int i = 0; i < PW / 4; ++i) {
                             const float4 k4 = ks[i], b4 = ks[TK / 4 + i];
-                            uint32_t* y = x + 4 * i;
-                            const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y)));
-                            const float2 z1 = unpack2(fma2(mul2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(k4.z, k4.w)), scale2, pack2(b4.z, b4.w)));
-                            y[0] = __float_as_uint(z0.x);
-                            y[1] = __float_as_uint(z0.y);
-                            y[2] = __float_as_uint(z1.x);
-                            y[3] = __float_as_uint(z1.y);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) {
+                                uint32_t* y = x[q] + 4 * i;
+                                const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2[q], pack2(b4.x, b4.y)));
+                                const float2 z1 = unpack2(fma2(mul2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(k4.z, k4.w)), scale2[q], pack2(b4.z, b4.w)));
+                                y[0] = __float_as_uint(z0.x);
+                                y[1] = __float_as_uint(z0.y);
+                                y[2] = __float_as_uint(z1.x);
+                                y[3] = __float_as_uint(z1.y);
+                            }
                         }
                         if (mask) {
 #pragma unroll
-                            for (int i = 0; i < PW; ++i)
-                                if (i < lo || i >= hi) x[i] = 0xff800000u;
+                            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                                for (int i = 0; i < PW; ++i)
+                                    if (i < lo[q] - PW * c || i >= hi[q] - PW * c) x[q][i] = 0xff800000u;
                         }
 #pragma unroll
-                        for (int i = 0; i < PW; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                        if (__any_sync(0xffffffffu, top > m + kMaxP)) {
-                            const float mn = fmaxf(m, ceilf(top) - kRaiseP);
-                            const float f = m == mn ? 1.f : ex2(m - mn);
-                            m = mn;
-                            m2 = m == -INFINITY ? 0ull : pack2(-m, -m);
-                            l *= f;
-                            l2 = mul2(l2, pack2(f, f));
+                        for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+                            for (int i = 0; i < PW; i += 2)
+                                top[q] = fmaxf(fmaxf(top[q], __uint_as_float(x[q][i])), __uint_as_float(x[q][i + 1]));
+                            s_row[met & 1][half][q][row] = top[q];
+                        }
+                        const int slot = met & 1;
+                        dead = !meet();
+                        if (dead) break;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            top[q] = fmaxf(top[q], s_row[slot][half ^ 1][q][row]);
+                            if (!__any_sync(0xffffffffu, top[q] > m[q] + kMaxP) || q >= nq) continue;
+                            const float mn = fmaxf(m[q], ceilf(top[q]) - kRaiseP);
+                            const float f = m[q] == mn ? 1.f : ex2(m[q] - mn);
+                            m[q] = mn;
+                            m2[q] = mn == -INFINITY ? 0ull : pack2(-mn, -mn);
+                            l[q] *= f;
+                            l2[q] = mul2(l2[q], pack2(f, f));
                             if (t > w.t0) {       // the sums of the earlier tiles are in tensor memory
-                                dead = !wait(&o_done[q], cnt - 1);
+                                dead = !wait(o_done, n - 1);
                                 dead = __any_sync(0xffffffffu, dead);
                                 if (dead) break;
                                 tc_fence_after();
                                 __syncwarp();
 #pragma unroll 1
-                                for (int d = 0; d < D / 16; ++d) {
+                                for (int d = half * (D / 32); d < (half + 1) * (D / 32); ++d) {
                                     uint32_t o[16];
-                                    tmem_ld_32x32b_x16(tO + 16 * d, o);
+                                    tmem_ld_32x32b_x16(tO + q * D + 16 * d, o);
                                     tmem_ld_wait();
 #pragma unroll
                                     for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tmem_st_32x32b_x16(tO + 16 * d, o);
+                                    tmem_st_32x32b_x16(tO + q * D + 16 * d, o);
                                 }
                             }
                             const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
-                            for (int d = 0; d < c * (PW / 32); ++d) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(tS + 16 * d, o);
+                            for (int d = 0; d < c * (PW / 16); ++d) {      // P of the earlier pieces
+                                const uint32_t at = tS + 2 * q * TK + half * CW + 8 * d;
+                                uint32_t o[8];
+                                tmem_ld_32x32b_x8(at, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
+                                for (int i = 0; i < 8; ++i) {
                                     const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), fh);
                                     o[i] = *reinterpret_cast<const uint32_t*>(&h);
                                 }
-                                tmem_st_32x32b_x16(tS + 16 * d, o);
+                                tmem_st_32x32b_x8(at, o);
                             }
                         }
+                        if (dead) break;
 #pragma unroll
-                        for (int g = 0; g < PW / 32; ++g) {
-                            uint32_t ph[16];
+                        for (int g = 0; g < PW / 16; ++g) {
+                            uint32_t ph[NQ][8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 i4 = ks[TK / 2 + 8 * g + i];
-                                const uint32_t* y = x + 32 * g + 4 * i;
-                                const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2));
-                                const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2));
-                                const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
-                                l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
-                                l2 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2);
-                                const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-                                ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
-                                ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 i4 = ks[TK / 2 + 4 * g + i];
+#pragma unroll
+                                for (int q = 0; q < NQ; ++q) {
+                                    const uint32_t* y = x[q] + 16 * g + 4 * i;
+                                    const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2[q]));
+                                    const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2[q]));
+                                    const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                                    l2[q] = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2[q]);
+                                    l2[q] = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2[q]);
+                                    const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+                                    ph[q][2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+                                    ph[q][2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                                }
                             }
-                            tmem_st_32x32b_x16(tS + 16 * (c * (PW / 32) + g), ph);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                tmem_st_32x32b_x8(tS + 2 * q * TK + half * CW + 8 * (c * (PW / 16) + g), ph[q]);
                         }
                     }
                     if (dead) break;
-                    const float2 ls = unpack2(l2);
-                    l += ls.x + ls.y;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const float2 ls = unpack2(l2[q]);
+                        l[q] += ls.x + ls.y;
+                    }
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -409,30 +509,33 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     }
                 }
                 if (dead) break;
-                dead = !wait(&o_done[q], cnt - 1);
+                const int slot = met & 1;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) s_row[slot][half][q][row] = l[q];
+                dead = !meet();
+                if (dead) break;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) l[q] += s_row[slot][half ^ 1][q][row];
+                dead = !wait(o_done, n - 1);
                 dead = __any_sync(0xffffffffu, dead);
                 if (dead) break;
                 tc_fence_after();
                 __syncwarp();
-            } else {
-                for (int t = w.t0; t < w.t1; ++t, ++n) {      // a query tile without rows only lets the scales go
-                    dead = !wait(&k_full[n & (NST - 1)], n >> kStLog2);
-                    dead = __any_sync(0xffffffffu, dead);
-                    if (dead) break;
-                    if (lane == 0) mbar_arrive(&sc_free[n & (NST - 1)]);
-                }
-                if (dead) break;
             }
-            if (active) {
-                const bool cut = w.u0 > 0 || w.u1 < w.it.tile.units;
-                const bool some = w.t0 < w.t1;
-                const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                float* part = p.part + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
+            // sums out: a warp has half of a row's columns
+            const bool cut = w.u0 > 0 || w.u1 < w.it.tile.units;
+            float* part = p.part + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const int r = q * 128 + row, last = w.n_rows - 1 - q * 128 - 32 * quad;    // the warp's last row
+                const bool live = r < w.n_rows;
+                if (last < 0) continue;
+                const float inv = cut ? 1.f : l[q] == 0.f ? 0.f : 1.f / l[q];
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
                     uint32_t o[32];
                     if (some) {
-                        tmem_ld_32x32b_x32(tO + 32 * c, o);
+                        tmem_ld_32x32b_x32(tO + q * D + 32 * c, o);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
@@ -447,39 +550,39 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     } else if (live) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {            // through the query tile's place, for whole-row stores
-                            const int ch = 4 * c + i;
                             uint32_t h[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 h[j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j]) * inv) |
                                        (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j + 1]) * inv) << 16;
-                            *reinterpret_cast<uint4*>(sq + q * C::kQBytes + row * 128 + (ch >> 3) * (128 * 128) +
-                                                      (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *place(q, lane, 4 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }
                     __syncwarp();
                 }
-                const int last = w.n_rows - 1 - q * 128 - 32 * (warp & 3);       // the warp's last row
-                if (!cut && last >= 0) {
-                    constexpr int LPR = D / 8, RPL = 32 / LPR;
+                if (!cut) {
+                    constexpr int LPR = D / 16, RPL = 32 / LPR;
 #pragma unroll 4
                     for (int i = 0; i < LPR; ++i) {
-                        const int rw = min(i * RPL + lane / LPR, last), ch = lane % LPR;   // (the last row: repeated)
-                        const int id = w.it.rt * C::kRows + q * 128 + 32 * (warp & 3) + rw;
+                        const int rw = min(i * RPL + lane / LPR, last), ch = half * LPR + lane % LPR;   // (the last row: repeated)
+                        const int id = row0 + q * 128 + 32 * quad + rw;
                         const size_t at = (size_t)(w.it.rows.q0 + id / p.G) * p.Hq + w.it.head * p.G + id % p.G;
-                        *(reinterpret_cast<uint4*>(p.out + at * D) + ch) = *reinterpret_cast<const uint4*>(
-                            sq + q * C::kQBytes + (32 * (warp & 3) + rw) * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rw & 7)) << 4));
+                        *(reinterpret_cast<uint4*>(p.out + at * D) + ch) = *place(q, rw, ch);
                     }
                     __syncwarp();
                 }
-                if (live && cut) {
-                    part[(size_t)C::kRows * D + r] = m;
-                    part[(size_t)C::kRows * (D + 1) + r] = l;
-                } else if (live && p.lse) {
-                    p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                if (live && half == 0) {
+                    const int id = row0 + r;
+                    if (cut) {
+                        part[(size_t)C::kRows * D + r] = m[q];
+                        part[(size_t)C::kRows * (D + 1) + r] = l[q];
+                    } else if (p.lse) {
+                        p.lse[(size_t)(w.it.rows.q0 + id / p.G) * p.Hq + w.it.head * p.G + id % p.G] =
+                            l[q] == 0.f ? -INFINITY : (m[q] + log2f(l[q])) * 0.6931471805599453f;
+                    }
                 }
-                tc_fence_before();      // O has been read before the next item's first P is announced
             }
+            tc_fence_before();      // O has been read before the next item's first P is announced
             if (threadIdx.x == 0) {
                 const bool goes_on = w.u0 == 0 && w.u1 < w.it.tile.units;
                 const Cut c = goes_on ? cut_of(line, w.it, w.x_end) : Cut{-1, 0, 0, 0};
@@ -491,22 +594,27 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
         // ------------------------------------------------------ images
         if (lane == 0) {
             uint32_t n = 0;
-            bool dead = false, half = false;     // half: only the keys of tile n are on their way
+            bool dead = false;
+            int half = 0;                        // of tile n on their way: 1 the keys, 2 the scales too
             while (more && !dead) {
                 const char* img = p.img + ((size_t)w.it.s * p.Hn + (w.it.head - p.h0)) * p.img_tiles * C::kImage;
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const char* src = img + (size_t)t * C::kImage;
                     const int st = n & (NST - 1);
                     const uint32_t ph = (n >> kStLog2) ^ 1;
-                    dead = !wait(&sc_free[st], ph) || !wait(&k_empty[st], ph);
+                    dead = !wait(&k_empty[st], ph);
                     if (dead) break;
-                    mbar_arrive_expect_tx(&k_full[st], (uint32_t)(C::kOpBytes + C::kScaleBytes));
+                    mbar_arrive_expect_tx(&k_full[st], (uint32_t)C::kOpBytes);
                     bulk_load(sk + st * C::kOpBytes, src, (uint32_t)C::kOpBytes, &k_full[st]);
-                    bulk_load(ssc + st * (C::kScaleBytes / 4), src + 2 * C::kOpBytes, (uint32_t)C::kScaleBytes, &k_full[st]);
-                    half = true;
+                    half = 1;
+                    dead = !wait(&sc_free[n & 3], (n >> 2) ^ 1);
+                    if (dead) break;
+                    mbar_arrive_expect_tx(&sc_full[n & 3], (uint32_t)C::kScaleBytes);
+                    bulk_load(ssc + (n & 3) * (C::kScaleBytes / 4), src + 2 * C::kOpBytes, (uint32_t)C::kScaleBytes, &sc_full[n & 3]);
+                    half = 2;
                     dead = !wait(&v_empty[st], ph);
                     if (dead) break;
-                    half = false;
+                    half = 0;
                     mbar_arrive_expect_tx(&v_full[st], (uint32_t)C::kOpBytes);
                     bulk_load(sv + st * C::kOpBytes, src + C::kOpBytes, (uint32_t)C::kOpBytes, &v_full[st]);
                 }
@@ -517,8 +625,10 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i) {
                 mbar_wait(&k_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
                 mbar_wait(&v_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
+                mbar_wait(&sc_full[i & 3], (i >> 2) & 1, &no_abort, kDrainLimit);
             }
-            if (half) mbar_wait(&k_full[n & (NST - 1)], (n >> kStLog2) & 1, &no_abort, kDrainLimit);
+            if (half > 0) mbar_wait(&k_full[n & (NST - 1)], (n >> kStLog2) & 1, &no_abort, kDrainLimit);
+            if (half > 1) mbar_wait(&sc_full[n & 3], (n >> 2) & 1, &no_abort, kDrainLimit);
         }
         __syncwarp();
     } else if (!IMG && warp < C::kMmaWarp) {
@@ -601,11 +711,11 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             locate();
             const int st = n & (NST - 1);
             const uint32_t ph = (n >> kStLog2) ^ 1;
-            bool dead = !wait(&empty[st], ph) || (keys && !wait(&sc_free[st], ph));
+            bool dead = !wait(&empty[st], ph) || (keys && !wait(&sc_free[n & 3], (n >> 2) ^ 1));
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             if (keys && tid < TK)
-                token_scales(p, !(cur.none >> 31), cur.ksc, cur.vsc, ssc + st * (C::kScaleBytes / 4) + tid, TK);
+                token_scales(p, !(cur.none >> 31), cur.ksc, cur.vsc, ssc + (n & 3) * (C::kScaleBytes / 4) + tid, TK);
             if (cur.none << 1) {                 // codes behind the last token may be anything, a NaN code too
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i)
@@ -625,71 +735,71 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
+            if (lane == 0) {
+                mbar_arrive(&full[st]);
+                if (keys) mbar_arrive(&sc_full[n & 3]);
+            }
             cur = next;
         }
     } else {
         // ------------------------------------------------------ issue
-        if (lane == 0) {
+        {
             const uint32_t idesc_s = idesc_f16(128, TK, 0), idesc_o = idesc_f16(128, D, 0) | kTransposeB;
-            const uint32_t q_base = smem_u32(sq), k_base = smem_u32(sk), v_base = smem_u32(sv);
+            const uint64_t q_desc = sdesc_k128(smem_u32(sq)), k_desc = sdesc_k128(smem_u32(sk)),
+                           v_desc = sdesc_mn128(smem_u32(sv), TK * 128);
             auto scores = [&](int q, int b, int st) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_f16(tmem + (2 * q + b) * TK, sdesc_k128(q_base + q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                             sdesc_k128(k_base + st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32), idesc_s, k > 0);
-                umma_commit(&s_full[2 * q + b]);
+                    mma_ss(tmem + (2 * q + b) * TK, q_desc + ((q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                           k_desc + ((st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0);
             };
+            // (each half's P lies over its own scores)
             auto sums = [&](int q, int b, int st, bool first) {
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k)
-                    umma_f16_ts(tmem + C::kColO + q * D, tmem + (2 * q + b) * TK + 8 * k,
-                                sdesc_mn128(v_base + st * C::kOpBytes + k * 2048, TK * 128), idesc_o, !first || k > 0);
-                umma_commit(&o_done[q]);
+                    mma_ts(tmem + C::kColO + q * D, tmem + (2 * q + b) * TK + (k >> 1) * (TK / 2) + (k & 1) * 8,
+                           v_desc + ((st * C::kOpBytes + k * 2048) >> 4), idesc_o, !first || k > 0);
             };
-            uint32_t n = 0, ns[2] = {0, 0}, np[2] = {0, 0}, qc[2] = {0, 0};   // tiles, and per query tile
+            auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+            uint32_t n = 0, items = 0;
             bool ok = true, issued = false;
             while (more && ok) {
-                const int J = w.t1 - w.t0;
-                const int nq = NQ == 2 && w.n_rows > 128 ? 2 : 1;
+                const int J = w.t1 - w.t0, nq = w.n_rows > 128 ? NQ : 1;
                 if (J > 0) {
-                    for (int q = 0; q < nq && ok; ++q) ok = wait(&q_full[q], qc[q]++);
-                    for (int j = -1; j < J && ok; ++j) {
-                        // the scores of the next tile first: the softmax finds them when it is done with this one's
-                        if (j + 1 < J) {
-                            const uint32_t m = n + (j >= 0 ? 1 : 0);
-                            const int st = m & (NST - 1);
-                            ok = wait(&k_full[st], m >> kStLog2);
+                    ok = wait_all(q_full, items++);
+                    // scores run two tiles ahead of the sums: those of tile j + 2 follow the sums of tile j, whose P
+                    // their buffer held, and are done while the softmax works on tile j + 1
+                    for (int j = -2; j < J && ok; ++j) {
+                        if (j >= 0) {
+                            const int st = n & (NST - 1);
+                            ok = wait_all(&v_full[st], n >> kStLog2) && wait_all(&p_full[n & 1], n >> 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            sums(0, n & 1, st, j == 0);
+                            if (nq == 2) sums(NQ - 1, n & 1, st, j == 0);
+                            commit(o_done);
+                            commit(&v_empty[st]);
+                        }
+                        if (j + 2 < J) {
+                            const uint32_t k = n + (j < 0 ? j + 2 : 2);
+                            const int st = k & (NST - 1);
+                            ok = wait_all(&k_full[st], k >> kStLog2);
                             if (!ok) break;
                             tc_fence_after();
                             issued = true;
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                if (q < nq) scores(q, ns[q]++ & 1, st);
-                            umma_commit(&k_empty[st]);
+                            scores(0, k & 1, st);
+                            if (nq == 2) scores(NQ - 1, k & 1, st);
+                            commit(&s_full[k & 1]);
+                            commit(&k_empty[st]);
                         }
-                        if (j < 0) continue;
-                        const int st = n & (NST - 1);
-                        ok = wait(&v_full[st], n >> kStLog2);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            if (q < nq && ok) {
-                                const int b = np[q] & 1;
-                                ok = wait(&p_full[2 * q + b], np[q]++ >> 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                                sums(q, b, st, j == 0);
-                            }
-                        if (!ok) break;
-                        umma_commit(&v_empty[st]);
-                        ++n;
+                        if (j >= 0) ++n;
                     }
                 }
                 if (ok) more = w.next(p, pl);
             }
             if (issued) {
                 // every MMA done before tensor memory is freed, even after an abort
-                umma_commit(final_bar);
+                commit(final_bar);
                 volatile int no_abort = 0;
                 mbar_wait(final_bar, 0, &no_abort, kWaitLimit);
             }
