@@ -8,7 +8,7 @@
 //   t_j = scale log2(e) a_j (q . ck_j) + log2(b_j),   p_j = 2^(t_j - m),
 //   out = sum_j p_j cv_j / sum_j p_j (1 / b_j).
 // Folding the value's scale into the exponent keeps the second product in
-// fp16 whatever the scales are: p is at most 2^14 (kMaxP) and the codes are
+// fp16 whatever the scales are: p is below 2^16 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
 // that of p to fp16 (half a step, 2^-12).  Queries are scaled by a power of
 // two per row into the fp16 range, which is exact; sums are fp32.

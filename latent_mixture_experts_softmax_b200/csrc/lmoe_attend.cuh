@@ -13,7 +13,7 @@ constexpr int kMaxCtas = 2 * kSms;
 // kRaiseP below the largest t.  P fits fp16 (2^16) with room, most key tiles
 // leave m as it is, and a p as small as 2^-126 still counts in the sum of a
 // row whose values' scales differ by 2^120.
-constexpr float kMaxP = 14.f, kRaiseP = 6.f;
+constexpr float kMaxP = 15.75f, kRaiseP = 6.f;
 constexpr int kFewRows = 32;            // query rows of an item of the kernel for few rows, at most
 
 // ---------------------------------------------------------------------------

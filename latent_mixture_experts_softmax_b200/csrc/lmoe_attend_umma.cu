@@ -9,11 +9,13 @@
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
 // 64 tokens:
-//   softmax      eight warps: a thread has a row of each query tile and half of
-//                the columns; S comes from tensor memory, P goes back over it
-//                as the A operand.  (Two rows a thread share the loads of the
-//                tokens' constants: shared memory, which feeds the tensor core
-//                as well, is what runs out first.)
+//   softmax      eight warps: a thread owns a row; S comes from tensor memory, P
+//                goes back over it as the A operand.  Four warps have a query
+//                tile each; where there is one tile, they take its key tiles in
+//                turn, handing on the row's reference.  (Warps that meet in
+//                every tile do the exponentials at the same time, and the units
+//                for those stand still in between: 2600 cycles a tile of 256
+//                rows.)
 //   keys, values four warps each read the codes of a tile (registers, one tile
 //                ahead) and write them as fp16 operands with the 128-byte
 //                swizzle; a key row is K-major as it is stored, and the same
@@ -41,7 +43,7 @@ namespace {
 using namespace sm100;
 using namespace attend;
 
-constexpr int kExtra = 4;                        // loading the queries and writing the sums, in key tiles
+constexpr int kExtra = 6;                        // loading the queries and writing the sums, in key tiles
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 constexpr uint64_t kDrainLimit = 20000000ull;    // and per wait for a copy in flight after one gave up
 
@@ -52,14 +54,14 @@ struct Many {
     static constexpr int NST = D == 256 ? 2 : 4;      // stages of keys, and of values
     static constexpr int kRows = NQ * 128;
     static constexpr int kKeyWarp = 8, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
-                         kMmaWarp = kValueWarp + (IMG ? 0 : 4);
+                         kMmaWarp = kValueWarp + (IMG ? 1 : 4);
     static constexpr int kThreads = (kMmaWarp + 1) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
     static constexpr size_t kImage = 2 * kOpBytes + kScaleBytes;   // keys, values, scales of a tile
     static constexpr size_t kSmem = 1024 + NQ * kQBytes + 2 * NST * kOpBytes + 4 * kScaleBytes + 512;
-    static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 ((2 q + b) * TK), sums from 256 (q * D)
+    static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 ((NB q + b) * TK), sums from 256 (q * D)
 };
 
 // MN-major operand: 64 elements of N (128 bytes, swizzled) by 8 of K per
@@ -113,27 +115,24 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
 // Contiguous bytes (16-byte aligned, a multiple of 16) to shared memory.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -209,10 +208,12 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     using C = Many<D, IMG>;
     constexpr int NQ = C::NQ, TK = C::TK, NST = C::NST;
     constexpr int kStLog2 = NST == 2 ? 1 : 2;
-    constexpr int CW = TK / 2;                   // columns of a softmax warp
-    constexpr int PW = IMG ? CW : 16;            // columns of a piece (registers: 168 a thread, or 96)
-    __shared__ float s_row[2][2][NQ][128];       // exchange between the two warps of a row
-    __shared__ float s_scale[NQ][128];
+    constexpr int NB = 4 / NQ;                   // score buffers of a query tile
+    constexpr int kBufLog2 = NB == 4 ? 2 : 1;
+    constexpr bool CH = NQ == 1;                 // two groups of softmax warps take one query tile's key tiles in turn
+    constexpr int PW = IMG ? TK : 32;            // columns of a piece (registers: 168 a thread, or 96)
+    __shared__ float s_m[2][CH ? 128 : 1];       // reference a key tile left, by the tile's parity
+    __shared__ float s_scale[CH ? 128 : 1], s_l[2][CH ? 128 : 1];
     extern __shared__ char smem_raw[];
     char* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
     char* sq = smem;
@@ -224,15 +225,16 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     uint64_t* v_full = bars + 4;     // [NST]
     uint64_t* k_empty = bars + 8;    // [NST] read by the tensor core (commit)
     uint64_t* v_empty = bars + 12;   // [NST]
-    uint64_t* sc_free = bars + 16;   // [4] scales of a stage read (8 warps)
-    uint64_t* s_full = bars + 20;    // [b] scores of a buffer done (commit)
-    uint64_t* p_full = bars + 22;    // [b] probabilities written (8 warps)
-    uint64_t* o_done = bars + 24;    // sums updated (commit)
-    uint64_t* q_full = bars + 25;    // query tiles written (8 warps)
-    uint64_t* sc_full = bars + 32;   // [4] scales of a stage written
-    uint64_t* pair = bars + 36;      // [4] the two warps of a row
+    uint64_t* sc_full = bars + 16;   // [4] scales of a stage written
+    uint64_t* sc_free = bars + 20;   // [4] and read
+    uint64_t* s_full = bars + 24;    // [NB q + b] scores of a buffer done (commit)
+    uint64_t* p_full = bars + 28;    // [NB q + b] probabilities written (4 warps)
+    uint64_t* o_done = bars + 32;    // [q] sums of a query tile updated (commit)
+    uint64_t* q_full = bars + 34;    // [q] query tile written
+    uint64_t* pair = bars + 36;      // [quad] CH: the two warps of a row meet
+    uint64_t* chain = bars + 41;     // [quad] CH: the reference of a key tile is known
     uint64_t* final_bar = bars + 40;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 41);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 45);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -243,15 +245,16 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
             mbar_init(&sc_full[i], IMG ? 1 : 4);
-            mbar_init(&sc_free[i], 8);
+            mbar_init(&sc_free[i], CH ? 4 : 8);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
             mbar_init(&pair[i], 2);
+            mbar_init(&chain[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 8);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&q_full[i], CH ? 8 : 4);
         }
-        mbar_init(o_done, 1);
-        mbar_init(q_full, 8);
         mbar_init(final_bar, 1);
         *abort_flag = 0;
         p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -283,9 +286,10 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     if (warp < 8) {
         // ------------------------------------------------------ softmax
         const int half = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
+        const int q = CH ? 0 : half;
         const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-        const uint32_t tO = tmem + lanes + C::kColO;
-        uint32_t n = 0;              // key tiles of the CTA
+        const uint32_t tO = tmem + lanes + C::kColO + q * D;
+        uint32_t n = 0, cnt = 0;     // key tiles of the CTA, and those of this query tile
         uint32_t met = 0;            // meetings of the two warps of a row
         bool dead = false;
         auto meet = [&]() {          // false: given up
@@ -294,40 +298,44 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             const bool ok = wait(&pair[quad], met++);
             return !__any_sync(0xffffffffu, !ok);
         };
-        // 16 bytes of a row of a query tile's place (fp16 queries, later bf16 sums)
-        auto place = [&](int q, int rw, int ch) {
+        // 16 bytes of a row of the query tile's place (fp16 queries, later bf16 sums)
+        auto place = [&](int rw, int ch) {
             return reinterpret_cast<uint4*>(sq + q * C::kQBytes + (32 * quad + rw) * 128 + (ch >> 3) * (128 * 128) +
                                             (((ch & 7) ^ (rw & 7)) << 4));
         };
         while (more && !dead) {
-            const int nq = w.n_rows > 128 ? NQ : 1;      // query tiles with rows
-            const int row0 = w.it.rt * C::kRows;
-            float m[NQ], l[NQ];
-            f2 m2[NQ];               // -m twice; 0 while m is -infinity
-            int pos[NQ];
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                m[q] = -INFINITY;
-                l[q] = 0.f;
-                m2[q] = 0ull;
-                pos[q] = w.it.rows.kv - w.it.rows.n + (row0 + q * 128 + row) / p.G;
-            }
+            const int r = q * 128 + row, row0 = w.it.rt * C::kRows;
             const bool some = w.t0 < w.t1;
+            // this thread's row: token and head (past the last row: that row)
+            const int tok = (row0 + min(r, w.n_rows - 1)) / p.G, gh = row0 + min(r, w.n_rows - 1) - tok * p.G;
+            const int pos = w.it.rows.kv - w.it.rows.n + tok;
+            const unsigned long long orow = (unsigned long long)(w.it.rows.q0 + tok) * p.Hq + w.it.head * p.G + gh;
+            float m = -INFINITY, l = 0.f;
+            if (q * 128 >= w.n_rows) {                           // a query tile without rows only lets the scales go
+                for (int t = w.t0; t < w.t1 && !dead; ++t, ++n) {
+                    dead = !wait(&sc_full[n & 3], n >> 2);
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (!dead && lane == 0) mbar_arrive(&sc_free[n & 3]);
+                }
+                if (!dead) more = w.next(p, pl);
+                continue;
+            }
             if (some) {
-                dead = !meet();      // both have stored the last item's sums from the tiles' places
-                if (dead) break;
-                // rows as fp16, each scaled by a power of two (past the last
-                // row: a copy of it, so that no load is conditional); the two
-                // warps take a tile each, or every other pass
+                if (CH) {
+                    dead = !meet();      // both have stored the last item's sums from the tile's place
+                    if (dead) break;
+                }
+                // the warp's rows as fp16, each scaled by a power of two (past
+                // the last row: a copy of it, so that no load is conditional);
+                // the two warps of a quarter take every other pass
                 constexpr int LPR = D / 8, RPL = 32 / LPR;       // lanes of a row, rows of a pass
-                const int qt = NQ == 2 ? half : 0;
+                const unsigned long long from =
+                    (unsigned long long)(w.it.rows.q0 + tok) * p.q_stride + (unsigned long long)(w.it.head * p.G + gh) * D;
+                float scale = 0.f;
 #pragma unroll 4
-                for (int i = NQ == 2 ? 0 : half; i < LPR; i += 3 - NQ) {
+                for (int i = CH ? half : 0; i < LPR; i += CH ? 2 : 1) {
                     const int rw = i * RPL + lane / LPR, ch = lane % LPR;
-                    const int id = row0 + min(qt * 128 + 32 * quad + rw, w.n_rows - 1);
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                                              p.q + (size_t)(w.it.rows.q0 + id / p.G) * p.q_stride +
-                                              (size_t)(w.it.head * p.G + id % p.G) * D) + ch);
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + __shfl_sync(0xffffffffu, from, rw)) + ch);
                     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
                     uint32_t mb = 0;
 #pragma unroll
@@ -337,9 +345,16 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     const bool bad = mb >= 0x7f80u;
                     const int e = min(max((int)(mb >> 7) - 127, -100), 126);
                     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-                    if (ch == 0)
-                        s_scale[qt][32 * quad + rw] =
-                            bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
+                    const float up = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (CH) {
+                        if (ch == 0) s_scale[32 * quad + rw] = up;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < RPL; ++j) {
+                            const float y = __shfl_sync(0xffffffffu, up, j * LPR);
+                            if (lane == i * RPL + j) scale = y;
+                        }
+                    }
                     uint32_t h[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -347,159 +362,134 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         const __half2 hh = __floats2half2_rn(f.x * down, f.y * down);
                         h[j] = bad ? 0u : *reinterpret_cast<const uint32_t*>(&hh);
                     }
-                    *place(qt, rw, ch) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *place(rw, ch) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-                dead = !meet();
-                if (dead) break;
-                f2 scale2[NQ];
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) scale2[q] = pack2(s_scale[q][row], s_scale[q][row]);
+                if (lane == 0) mbar_arrive(&q_full[q]);
+                if (CH) {
+                    dead = !meet();
+                    if (dead) break;
+                    scale = s_scale[row];
+                }
+                const f2 scale2 = pack2(scale, scale);
 
-                for (int t = w.t0; t < w.t1; ++t, ++n) {
-                    const int st = n & 3, b = n & 1;
-                    dead = !wait(&sc_full[st], n >> 2) || !wait(&s_full[b], n >> 1);
+                for (int t = w.t0; t < w.t1; ++t, ++n, ++cnt) {
+                    if (CH && (int)(n & 1) != half) continue;
+                    const int st = n & 3, b = NB * q + (cnt & (NB - 1));
+                    dead = !wait(&sc_full[st], n >> 2) || !wait(&s_full[b], cnt >> kBufLog2);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     tc_fence_after();
                     __syncwarp();
-                    const uint32_t tS = tmem + lanes + b * TK;       // (query tile q: 2 q TK on)
-                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4) + half * CW);
-                    const int tok0 = t * TK + half * CW;
-                    // keys a row sees: columns lo .. hi - 1
-                    int hi[NQ], lo[NQ];
-                    bool edge = false;
+                    const uint32_t tS = tmem + lanes + b * TK;
+                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
+                    const int tok0 = t * TK;
+                    // keys this row sees: columns lo .. hi - 1
+                    const int hi = p.causal ? pos + 1 - tok0 : TK;
+                    const int lo = p.window ? pos + 1 - p.window - tok0 : 0;
+                    const bool mask = __any_sync(0xffffffffu, hi < TK || lo > 0);
+                    uint32_t x[PW];
+                    auto exponents = [&](int c) {        // piece c of t_j
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        hi[q] = p.causal ? pos[q] + 1 - tok0 : CW;
-                        lo[q] = p.window ? pos[q] + 1 - p.window - tok0 : 0;
-                        edge |= hi[q] < CW || lo[q] > 0;
-                    }
-                    const bool mask = __any_sync(0xffffffffu, edge);
-                    f2 l2[NQ];
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) l2[q] = pack2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < CW / PW; ++c, ks += PW / 4) {
-                        uint32_t x[NQ][PW];
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                            for (int i = 0; i < PW / 16; ++i)
-                                tmem_ld_32x32b_x16(tS + 2 * q * TK + half * CW + PW * c + 16 * i,
-                                                   *reinterpret_cast<uint32_t(*)[16]>(x[q] + 16 * i));
+                        for (int i = 0; i < PW / 32; ++i)
+                            tmem_ld_32x32b_x32(tS + PW * c + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * i));
                         tmem_ld_wait();
-                        float top[NQ];
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) top[q] = -INFINITY;
-                        // the tokens' constants come from shared memory, whose
-                        // bandwidth the tensor core's operands need most of:
-                        // one load serves both query tiles
 #pragma unroll
                         for (int i = 0; i < PW / 4; ++i) {
-                            const float4 k4 = ks[i], b4 = ks[TK / 4 + i];
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q) {
-                                uint32_t* y = x[q] + 4 * i;
-                                const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2[q], pack2(b4.x, b4.y)));
-                                const float2 z1 = unpack2(fma2(mul2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(k4.z, k4.w)), scale2[q], pack2(b4.z, b4.w)));
-                                y[0] = __float_as_uint(z0.x);
-                                y[1] = __float_as_uint(z0.y);
-                                y[2] = __float_as_uint(z1.x);
-                                y[3] = __float_as_uint(z1.y);
-                            }
+                            const float4 k4 = ks[PW / 4 * c + i], b4 = ks[TK / 4 + PW / 4 * c + i];
+                            uint32_t* y = x + 4 * i;
+                            const float2 z0 = unpack2(fma2(mul2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), pack2(k4.x, k4.y)), scale2, pack2(b4.x, b4.y)));
+                            const float2 z1 = unpack2(fma2(mul2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), pack2(k4.z, k4.w)), scale2, pack2(b4.z, b4.w)));
+                            y[0] = __float_as_uint(z0.x);
+                            y[1] = __float_as_uint(z0.y);
+                            y[2] = __float_as_uint(z1.x);
+                            y[3] = __float_as_uint(z1.y);
                         }
                         if (mask) {
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-#pragma unroll
-                                for (int i = 0; i < PW; ++i)
-                                    if (i < lo[q] - PW * c || i >= hi[q] - PW * c) x[q][i] = 0xff800000u;
+                            for (int i = 0; i < PW; ++i)
+                                if (PW * c + i < lo || PW * c + i >= hi) x[i] = 0xff800000u;
                         }
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-#pragma unroll
-                            for (int i = 0; i < PW; i += 2)
-                                top[q] = fmaxf(fmaxf(top[q], __uint_as_float(x[q][i])), __uint_as_float(x[q][i + 1]));
-                            s_row[met & 1][half][q][row] = top[q];
-                        }
-                        const int slot = met & 1;
-                        dead = !meet();
-                        if (dead) break;
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            top[q] = fmaxf(top[q], s_row[slot][half ^ 1][q][row]);
-                            if (!__any_sync(0xffffffffu, top[q] > m[q] + kMaxP) || q >= nq) continue;
-                            const float mn = fmaxf(m[q], ceilf(top[q]) - kRaiseP);
-                            const float f = m[q] == mn ? 1.f : ex2(m[q] - mn);
-                            m[q] = mn;
-                            m2[q] = mn == -INFINITY ? 0ull : pack2(-mn, -mn);
-                            l[q] *= f;
-                            l2[q] = mul2(l2[q], pack2(f, f));
-                            if (t > w.t0) {       // the sums of the earlier tiles are in tensor memory
-                                dead = !wait(o_done, n - 1);
-                                dead = __any_sync(0xffffffffu, dead);
-                                if (dead) break;
-                                tc_fence_after();
-                                __syncwarp();
+                    };
+                    float top = -INFINITY;
 #pragma unroll 1
-                                for (int d = half * (D / 32); d < (half + 1) * (D / 32); ++d) {
-                                    uint32_t o[16];
-                                    tmem_ld_32x32b_x16(tO + q * D + 16 * d, o);
-                                    tmem_ld_wait();
+                    for (int c = 0; c < TK / PW; ++c) {
+                        exponents(c);
+                        float a = -INFINITY;
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tmem_st_32x32b_x16(tO + q * D + 16 * d, o);
-                                }
-                            }
-                            const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-                            for (int d = 0; d < c * (PW / 16); ++d) {      // P of the earlier pieces
-                                const uint32_t at = tS + 2 * q * TK + half * CW + 8 * d;
-                                uint32_t o[8];
-                                tmem_ld_32x32b_x8(at, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), fh);
-                                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-                                }
-                                tmem_st_32x32b_x8(at, o);
-                            }
+                        for (int i = 0; i < PW; i += 4) {
+                            top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                            a = fmaxf(fmaxf(a, __uint_as_float(x[i + 2])), __uint_as_float(x[i + 3]));
                         }
-                        if (dead) break;
-#pragma unroll
-                        for (int g = 0; g < PW / 16; ++g) {
-                            uint32_t ph[NQ][8];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 i4 = ks[TK / 2 + 4 * g + i];
-#pragma unroll
-                                for (int q = 0; q < NQ; ++q) {
-                                    const uint32_t* y = x[q] + 16 * g + 4 * i;
-                                    const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2[q]));
-                                    const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2[q]));
-                                    const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
-                                    l2[q] = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2[q]);
-                                    l2[q] = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l2[q]);
-                                    const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
-                                    ph[q][2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
-                                    ph[q][2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                                }
-                            }
-#pragma unroll
-                            for (int q = 0; q < NQ; ++q)
-                                tmem_st_32x32b_x8(tS + 2 * q * TK + half * CW + 8 * (c * (PW / 16) + g), ph[q]);
+                        top = fmaxf(top, a);
+                    }
+                    float was = m;                       // the reference of the tile before
+                    if (CH) {
+                        was = -INFINITY;
+                        if (t > w.t0) {
+                            dead = !wait(&chain[quad], n - 1);
+                            dead = __any_sync(0xffffffffu, dead);
+                            if (dead) break;
+                            was = s_m[(n - 1) & 1][row];
                         }
                     }
-                    if (dead) break;
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        const float2 ls = unpack2(l2[q]);
-                        l[q] += ls.x + ls.y;
+                    float now = was;
+                    const bool grow = __any_sync(0xffffffffu, top > was + kMaxP);
+                    if (grow) now = fmaxf(was, ceilf(top) - kRaiseP);
+                    if (CH) {
+                        s_m[n & 1][row] = now;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&chain[quad]);
                     }
+                    if (__any_sync(0xffffffffu, m != now)) {     // (CH: also where the other warp has raised it)
+                        l *= m == now ? 1.f : ex2(m - now);
+                        m = now;
+                    }
+                    if (grow && t > w.t0) {              // the sums of the earlier tiles are in tensor memory
+                        const float f = was == now ? 1.f : ex2(was - now);
+                        dead = !wait(&o_done[q], cnt - 1);
+                        dead = __any_sync(0xffffffffu, dead);
+                        if (dead) break;
+                        tc_fence_after();
+                        __syncwarp();
+#pragma unroll 1
+                        for (int d = 0; d < D / 32; ++d) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(tO + 32 * d, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st_32x32b_x32(tO + 32 * d, o);
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : -m;
+                    const f2 m2 = pack2(mm, mm);
+                    f2 l2 = pack2(0.f, 0.f), l3 = pack2(0.f, 0.f);
+#pragma unroll 1
+                    for (int c = 0; c < TK / PW; ++c) {
+                        if (!IMG) exponents(c);          // (fewer registers: gone through twice)
+#pragma unroll
+                        for (int g = 0; g < PW / 32; ++g) {
+                            uint32_t ph[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 i4 = ks[TK / 2 + PW / 4 * c + 8 * g + i];
+                                const uint32_t* y = x + 32 * g + 4 * i;
+                                const float2 y0 = unpack2(add2(pack2(__uint_as_float(y[0]), __uint_as_float(y[1])), m2));
+                                const float2 y1 = unpack2(add2(pack2(__uint_as_float(y[2]), __uint_as_float(y[3])), m2));
+                                const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                                l2 = fma2(pack2(p0, p1), pack2(i4.x, i4.y), l2);
+                                l3 = fma2(pack2(p2, p3), pack2(i4.z, i4.w), l3);
+                                const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+                                ph[2 * i] = *reinterpret_cast<const uint32_t*>(&h0);
+                                ph[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                            }
+                            tmem_st_32x32b_x16(tS + 16 * (c * (PW / 32) + g), ph);
+                        }
+                    }
+                    const float2 la = unpack2(l2), lb = unpack2(l3);
+                    l += (la.x + la.y) + (lb.x + lb.y);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -509,33 +499,37 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     }
                 }
                 if (dead) break;
-                const int slot = met & 1;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) s_row[slot][half][q][row] = l[q];
-                dead = !meet();
-                if (dead) break;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) l[q] += s_row[slot][half ^ 1][q][row];
-                dead = !wait(o_done, n - 1);
+                if (CH) {
+                    dead = !wait(&chain[quad], n - 1);
+                    dead = __any_sync(0xffffffffu, dead);
+                    if (dead) break;
+                    const float now = s_m[(n - 1) & 1][row];
+                    s_l[half][row] = l *= m == now ? 1.f : ex2(m - now);
+                    m = now;
+                    dead = !meet();
+                    if (dead) break;
+                    l = s_l[0][row] + s_l[1][row];
+                }
+                dead = !wait(&o_done[q], cnt - 1);
                 dead = __any_sync(0xffffffffu, dead);
                 if (dead) break;
                 tc_fence_after();
                 __syncwarp();
             }
-            // sums out: a warp has half of a row's columns
+            // sums out (CH: a warp has half of its rows' columns)
+            constexpr int SP = CH ? 2 : 1;
+            const int part_of = CH ? half : 0;
             const bool cut = w.u0 > 0 || w.u1 < w.it.tile.units;
+            const bool live = r < w.n_rows;
             float* part = p.part + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-                const int r = q * 128 + row, last = w.n_rows - 1 - q * 128 - 32 * quad;    // the warp's last row
-                const bool live = r < w.n_rows;
-                if (last < 0) continue;
-                const float inv = cut ? 1.f : l[q] == 0.f ? 0.f : 1.f / l[q];
+            const int last = w.n_rows - 1 - q * 128 - 32 * quad;     // the warp's last row
+            if (last >= 0) {
+                const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+                for (int c = part_of * (D / 32 / SP); c < (part_of + 1) * (D / 32 / SP); ++c) {
                     uint32_t o[32];
                     if (some) {
-                        tmem_ld_32x32b_x32(tO + q * D + 32 * c, o);
+                        tmem_ld_32x32b_x32(tO + 32 * c, o);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
@@ -553,32 +547,28 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                             uint32_t h[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                h[j] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j]) * inv) |
-                                       (uint32_t)f32_to_bf16_bits(__uint_as_float(o[8 * i + 2 * j + 1]) * inv) << 16;
-                            *place(q, lane, 4 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
+                                h[j] = bf16x2_of(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
+                            *place(lane, 4 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }
                     __syncwarp();
                 }
                 if (!cut) {
-                    constexpr int LPR = D / 16, RPL = 32 / LPR;
+                    constexpr int LPR = D / 8 / SP, RPL = 32 / LPR;
 #pragma unroll 4
                     for (int i = 0; i < LPR; ++i) {
-                        const int rw = min(i * RPL + lane / LPR, last), ch = half * LPR + lane % LPR;   // (the last row: repeated)
-                        const int id = row0 + q * 128 + 32 * quad + rw;
-                        const size_t at = (size_t)(w.it.rows.q0 + id / p.G) * p.Hq + w.it.head * p.G + id % p.G;
-                        *(reinterpret_cast<uint4*>(p.out + at * D) + ch) = *place(q, rw, ch);
+                        const int rw = min(i * RPL + lane / LPR, last), ch = part_of * LPR + lane % LPR;   // (the last row: repeated)
+                        const unsigned long long at = __shfl_sync(0xffffffffu, orow, rw);
+                        *(reinterpret_cast<uint4*>(p.out + at * D) + ch) = *place(rw, ch);
                     }
                     __syncwarp();
                 }
-                if (live && half == 0) {
-                    const int id = row0 + r;
+                if (live && part_of == 0) {
                     if (cut) {
-                        part[(size_t)C::kRows * D + r] = m[q];
-                        part[(size_t)C::kRows * (D + 1) + r] = l[q];
+                        part[(size_t)C::kRows * D + r] = m;
+                        part[(size_t)C::kRows * (D + 1) + r] = l;
                     } else if (p.lse) {
-                        p.lse[(size_t)(w.it.rows.q0 + id / p.G) * p.Hq + w.it.head * p.G + id % p.G] =
-                            l[q] == 0.f ? -INFINITY : (m[q] + log2f(l[q])) * 0.6931471805599453f;
+                        p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     }
                 }
             }
@@ -593,42 +583,44 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     } else if (IMG && warp < C::kMmaWarp) {
         // ------------------------------------------------------ images
         if (lane == 0) {
+            const bool keys = warp == C::kKeyWarp;
             uint32_t n = 0;
-            bool dead = false;
-            int half = 0;                        // of tile n on their way: 1 the keys, 2 the scales too
+            bool dead = false, half = false;     // half: the scales of tile n are on their way
+            grid_dep_wait();                     // the images are written
             while (more && !dead) {
                 const char* img = p.img + ((size_t)w.it.s * p.Hn + (w.it.head - p.h0)) * p.img_tiles * C::kImage;
                 for (int t = w.t0; t < w.t1; ++t, ++n) {
                     const char* src = img + (size_t)t * C::kImage;
                     const int st = n & (NST - 1);
                     const uint32_t ph = (n >> kStLog2) ^ 1;
-                    dead = !wait(&k_empty[st], ph);
-                    if (dead) break;
-                    mbar_arrive_expect_tx(&k_full[st], (uint32_t)C::kOpBytes);
-                    bulk_load(sk + st * C::kOpBytes, src, (uint32_t)C::kOpBytes, &k_full[st]);
-                    half = 1;
-                    dead = !wait(&sc_free[n & 3], (n >> 2) ^ 1);
-                    if (dead) break;
-                    mbar_arrive_expect_tx(&sc_full[n & 3], (uint32_t)C::kScaleBytes);
-                    bulk_load(ssc + (n & 3) * (C::kScaleBytes / 4), src + 2 * C::kOpBytes, (uint32_t)C::kScaleBytes, &sc_full[n & 3]);
-                    half = 2;
-                    dead = !wait(&v_empty[st], ph);
-                    if (dead) break;
-                    half = 0;
-                    mbar_arrive_expect_tx(&v_full[st], (uint32_t)C::kOpBytes);
-                    bulk_load(sv + st * C::kOpBytes, src + C::kOpBytes, (uint32_t)C::kOpBytes, &v_full[st]);
+                    if (keys) {
+                        dead = !wait(&sc_free[n & 3], (n >> 2) ^ 1);
+                        if (dead) break;
+                        mbar_arrive_expect_tx(&sc_full[n & 3], (uint32_t)C::kScaleBytes);
+                        bulk_load(ssc + (n & 3) * (C::kScaleBytes / 4), src + 2 * C::kOpBytes, (uint32_t)C::kScaleBytes, &sc_full[n & 3]);
+                        half = true;
+                        dead = !wait(&k_empty[st], ph);
+                        if (dead) break;
+                        half = false;
+                        mbar_arrive_expect_tx(&k_full[st], (uint32_t)C::kOpBytes);
+                        bulk_load(sk + st * C::kOpBytes, src, (uint32_t)C::kOpBytes, &k_full[st]);
+                    } else {
+                        dead = !wait(&v_empty[st], ph);
+                        if (dead) break;
+                        mbar_arrive_expect_tx(&v_full[st], (uint32_t)C::kOpBytes);
+                        bulk_load(sv + st * C::kOpBytes, src + C::kOpBytes, (uint32_t)C::kOpBytes, &v_full[st]);
+                    }
                 }
                 if (!dead) more = w.next(p, pl);
             }
             // the copies in flight end before the CTA does, after an abort too
             volatile int no_abort = 0;
-            for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i) {
-                mbar_wait(&k_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
-                mbar_wait(&v_full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
-                mbar_wait(&sc_full[i & 3], (i >> 2) & 1, &no_abort, kDrainLimit);
-            }
-            if (half > 0) mbar_wait(&k_full[n & (NST - 1)], (n >> kStLog2) & 1, &no_abort, kDrainLimit);
-            if (half > 1) mbar_wait(&sc_full[n & 3], (n >> 2) & 1, &no_abort, kDrainLimit);
+            uint64_t* full = keys ? k_full : v_full;
+            for (uint32_t i = n > NST ? n - NST : 0; i < n; ++i)
+                mbar_wait(&full[i & (NST - 1)], (i >> kStLog2) & 1, &no_abort, kDrainLimit);
+            if (keys)
+                for (uint32_t i = n > 3 ? n - 3 : 0; i < n + (half ? 1 : 0); ++i)
+                    mbar_wait(&sc_full[i & 3], (i >> 2) & 1, &no_abort, kDrainLimit);
         }
         __syncwarp();
     } else if (!IMG && warp < C::kMmaWarp) {
@@ -750,49 +742,61 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             auto scores = [&](int q, int b, int st) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + (2 * q + b) * TK, q_desc + ((q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                    mma_ss(tmem + (NB * q + b) * TK, q_desc + ((q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
                            k_desc + ((st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0);
             };
-            // (each half's P lies over its own scores)
             auto sums = [&](int q, int b, int st, bool first) {
 #pragma unroll
                 for (int k = 0; k < TK / 16; ++k)
-                    mma_ts(tmem + C::kColO + q * D, tmem + (2 * q + b) * TK + (k >> 1) * (TK / 2) + (k & 1) * 8,
+                    mma_ts(tmem + C::kColO + q * D, tmem + (NB * q + b) * TK + k * 8,
                            v_desc + ((st * C::kOpBytes + k * 2048) >> 4), idesc_o, !first || k > 0);
             };
             auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-            uint32_t n = 0, items = 0;
+            uint32_t n = 0, ns[2] = {0, 0}, np[2] = {0, 0}, qc[2] = {0, 0};   // tiles, and per query tile
             bool ok = true, issued = false;
             while (more && ok) {
                 const int J = w.t1 - w.t0, nq = w.n_rows > 128 ? NQ : 1;
                 if (J > 0) {
-                    ok = wait_all(q_full, items++);
-                    // scores run two tiles ahead of the sums: those of tile j + 2 follow the sums of tile j, whose P
-                    // their buffer held, and are done while the softmax works on tile j + 1
+                    for (int q = 0; q < nq && ok; ++q) ok = wait_all(&q_full[q], qc[q]++);
+                    // scores run two tiles ahead of the sums.  Two buffers: those of tile j + 2 follow the sums of
+                    // tile j, whose P their buffer held; four: they go before them
                     for (int j = -2; j < J && ok; ++j) {
-                        if (j >= 0) {
-                            const int st = n & (NST - 1);
-                            ok = wait_all(&v_full[st], n >> kStLog2) && wait_all(&p_full[n & 1], n >> 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            sums(0, n & 1, st, j == 0);
-                            if (nq == 2) sums(NQ - 1, n & 1, st, j == 0);
-                            commit(o_done);
-                            commit(&v_empty[st]);
-                        }
-                        if (j + 2 < J) {
-                            const uint32_t k = n + (j < 0 ? j + 2 : 2);
-                            const int st = k & (NST - 1);
-                            ok = wait_all(&k_full[st], k >> kStLog2);
-                            if (!ok) break;
+                        const bool ahead = j + 2 < J;
+                        const uint32_t k = n + (j < 0 ? j + 2 : 2);
+                        const int st = n & (NST - 1), st2 = k & (NST - 1);
+                        auto score = [&](int q) {
+                            if (q == 0) ok = wait_all(&k_full[st2], k >> kStLog2);
+                            if (!ok) return;
                             tc_fence_after();
                             issued = true;
-                            scores(0, k & 1, st);
-                            if (nq == 2) scores(NQ - 1, k & 1, st);
-                            commit(&s_full[k & 1]);
-                            commit(&k_empty[st]);
+                            const int b = ns[q]++ & (NB - 1);
+                            scores(q, b, st2);
+                            commit(&s_full[NB * q + b]);
+                        };
+                        if (NB == 4 && ahead) {
+                            score(0);
+                            if (ok) commit(&k_empty[st2]);
                         }
-                        if (j >= 0) ++n;
+                        if (j >= 0 && ok) ok = wait_all(&v_full[st], n >> kStLog2);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            if (q < nq && ok) {
+                                if (j >= 0) {
+                                    const int b = np[q] & (NB - 1);
+                                    ok = wait_all(&p_full[NB * q + b], np[q]++ >> kBufLog2);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    sums(q, b, st, j == 0);
+                                    commit(&o_done[q]);
+                                }
+                                if (NB == 2 && ahead) score(q);
+                            }
+                        if (!ok) break;
+                        if (NB == 2 && ahead) commit(&k_empty[st2]);
+                        if (j >= 0) {
+                            commit(&v_empty[st]);
+                            ++n;
+                        }
                     }
                 }
                 if (ok) more = w.next(p, pl);
@@ -829,6 +833,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(256) k_attend_images(AttendParams p) {
     using C = Many<D, true>;
     constexpr int TK = C::TK, BLKS = D / 64, RPP = 64 / BLKS;      // rows of a pass
+    sm100::grid_dep_launch();
     const SeqRows r = seq_rows(p, blockIdx.z);
     if (r.n <= 0) return;
     const int first = r.kv - r.n, lo = p.window ? max(0, first - p.window + 1) : 0;
@@ -884,8 +889,18 @@ cudaError_t launch(const AttendParams& p, cudaStream_t st) {
     const Plan pl{C::kRows, 6, 1, kExtra};
     cudaError_t e = allow_smem<k_attend_many<D, FMT, IMG>>(C::kSmem);
     if (e != cudaSuccess) return e;
-    k_attend_many<D, FMT, IMG><<<kSms, C::kThreads, C::kSmem, st>>>(p, pl);
-    e = cudaGetLastError();
+    // over the images' kernel: it starts while that one runs, and its loaders wait for it
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kSms);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = IMG ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, k_attend_many<D, FMT, IMG>, p, pl);
     if (e != cudaSuccess) return e;
     return launch_join(p, C::kRows, kSms, false, st);
 }
