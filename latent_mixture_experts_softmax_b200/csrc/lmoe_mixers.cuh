@@ -108,7 +108,7 @@ cudaError_t run_kv_read(const KvParams& p, uint16_t* k, uint16_t* v, size_t k_st
                         cudaStream_t st);
 size_t attend_ws_bytes(int D);
 cudaError_t run_attend(AttendParams p, void* ws, cudaStream_t st);
-size_t delta_chunk_ws_bytes(int H, int DK, int DV, int n_tokens, int n_seqs, int max_new);
+size_t delta_chunk_ws_bytes(int H, int n_tokens, int n_seqs, int max_new);
 cudaError_t run_delta(const DeltaParams& p, cudaStream_t st);
 
 }  // namespace lmoe

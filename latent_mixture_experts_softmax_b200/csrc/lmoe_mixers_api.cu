@@ -80,7 +80,7 @@ int check_delta(const lmoe_delta_cfg* c) {
 }
 
 size_t delta_ws(const lmoe_delta_cfg& c, int n_tokens, int n_seqs, int max_new) {
-    return kAttnCtrlBytes + delta_chunk_ws_bytes(c.n_heads, c.head_k, c.head_v, n_tokens, n_seqs, max_new);
+    return kAttnCtrlBytes + delta_chunk_ws_bytes(c.n_heads, n_tokens, n_seqs, max_new);
 }
 
 }  // namespace
