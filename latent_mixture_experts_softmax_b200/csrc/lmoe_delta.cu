@@ -161,13 +161,14 @@ __global__ void __launch_bounds__(kStepWarps * 32) k_delta_step(DeltaParams p) {
 
 constexpr int kC = 32;                       // tokens of a chunk
 
-// What k_delta_chunks leaves of a chunk and head.  A fragment: 16 bytes per
-// lane, an m16 x k16 operand; tiles (0, 0), (1, 0), (1, 1) of the 32 x 32.
+// What k_delta_chunks leaves of a chunk and head.  T and P as the second
+// operand of a product: tile (k, j), 16 x 8, holds rows 8 j .. of the matrix at
+// columns 16 k .. (tiles that are not zero: 0..3 = (0, j), 4, 5 = (1, 2), (1, 3)),
+// 16 bytes a lane: the two registers of the high terms, then of the low.
 struct ChunkData {
-    uint4 t[3][2][32];                       // [tile][high, low][lane]
-    uint4 p[3][2][32];
-    float4 f[kC];                            // b, b exp(G) |k|^-1, scale exp(G) |q|^-1, exp(G_C - G) |k|^-1
-    float4 last;                             // exp(G_C)
+    uint4 t[6][32], p[6][32];
+    float b[kC], kf[kC], qf[kC], wf[kC];     // b, b exp(G) |k|^-1, scale exp(G) |q|^-1, exp(G_C - G) |k|^-1
+    float last[4];                           // exp(G_C)
 };
 
 __host__ __device__ __forceinline__ int chunks_of(int n) { return (n + kC - 1) / kC; }
@@ -195,7 +196,7 @@ __device__ DeltaRows chunk_rows(const DeltaParams& p, int s, int slots, int* bas
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -228,51 +229,39 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows of a chunk (n_here of them, zeros behind) of one head to shared memory.
-template <int DK>
-__device__ __forceinline__ void load_rows(uint16_t (*dst)[DK + 8], const uint16_t* src, size_t stride, int n_here, int nt) {
-    for (int i = threadIdx.x; i < kC * DK / 8; i += nt) {
-        const int r = i / (DK / 8), c = i % (DK / 8) * 8;
-        if (r < n_here) cp_async16(&dst[r][c], src + (size_t)r * stride + c);
-        else *reinterpret_cast<uint4*>(&dst[r][c]) = make_uint4(0, 0, 0, 0);
+// W elements of each row of a chunk (n_here rows, zeros behind) to shared memory.
+template <int W, int STRIDE>
+__device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, size_t stride, int n_here, int nt) {
+#pragma unroll
+    for (int i0 = 0; i0 < kC * W / 8; i0 += nt) {
+        const int i = i0 + threadIdx.x;
+        const int r = i / (W / 8), c = i % (W / 8) * 8;
+        if (r < n_here) cp_async16(dst + r * STRIDE + c, src + (size_t)r * stride + c);
+        else *reinterpret_cast<uint4*>(dst + r * STRIDE + c) = make_uint4(0, 0, 0, 0);
     }
 }
 
 constexpr int kPrepThreads = 128;
 
-// Block (chunk, head, sequence).
+// Block (chunk, head of q and k, sequence).  K K^T and Q K^T once, then two of
+// the heads that share them at a time, two warps each: one for T, one for P
+// and the factors.
 template <int DK>
 __global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, int slots) {
     __shared__ __align__(16) uint16_t sk[kC][DK + 8], sq[kC][DK + 8];
-    __shared__ __align__(16) float sa[kC][kC + 4], sp[kC][kC + 4];
-    __shared__ float s_rk[kC], s_rq[kC], s_b[kC], s_gh[kC], s_gl[kC];
+    __shared__ __align__(16) float kk[kC][kC + 4], qk[kC][kC + 4], sa[2][kC][kC + 4];
+    __shared__ float s_rk[kC], s_rq[kC], s_gh[4][kC], s_gl[4][kC];
     sm100::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int h = blockIdx.y, hq = h / p.group;
+    const int hq = blockIdx.y;
     for (int s = blockIdx.z; s < p.n_seqs; s += gridDim.z) {
         int base;
         const DeltaRows r = chunk_rows(p, s, slots, &base);
         if (r.n <= 0 || (int)blockIdx.x >= chunks_of(r.n)) continue;
         const int row0 = r.q0 + blockIdx.x * kC, n_here = min(kC, r.n - (int)blockIdx.x * kC);
-        load_rows<DK>(sk, p.k + (size_t)row0 * p.ks + (size_t)hq * DK, p.ks, n_here, kPrepThreads);
-        load_rows<DK>(sq, p.q + (size_t)row0 * p.qs + (size_t)hq * DK, p.qs, n_here, kPrepThreads);
+        load_rows<DK, DK + 8>(&sk[0][0], p.k + (size_t)row0 * p.ks + (size_t)hq * DK, p.ks, n_here, kPrepThreads);
+        load_rows<DK, DK + 8>(&sq[0][0], p.q + (size_t)row0 * p.qs + (size_t)hq * DK, p.qs, n_here, kPrepThreads);
         cp_async_commit();
-        if (warp == 0) {
-            // decays: a sum in two parts, multiples of 1/8 (exact) and the
-            // rest (small), so that differences of large sums stay exact
-            const size_t at = (size_t)(row0 + min(lane, n_here - 1)) * p.H + h;
-            float gt = lane < n_here ? p.log_decay[at] : 0.f;
-            if (gt < -128.f) gt = -128.f;                        // (-infinity too: e^-128 is 0 in fp32)
-            float gh = rintf(gt * 8.f) * 0.125f, gl = gt - gh;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float yh = __shfl_up_sync(0xffffffffu, gh, o), yl = __shfl_up_sync(0xffffffffu, gl, o);
-                if (lane >= o) { gh += yh; gl += yl; }
-            }
-            s_gh[lane] = gh;
-            s_gl[lane] = gl;
-            s_b[lane] = lane < n_here ? p.beta[at] : 0.f;
-        }
         cp_async_wait<0>();
         __syncthreads();
         // norms: four threads a row
@@ -296,7 +285,6 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, in
                 s_rq[row] = p.scale * (p.l2norm ? 1.f / sqrtf(nq + 1e-6f) : 1.f);
             }
         }
-        __syncthreads();
         // K K^T (warps 0, 1) and Q K^T (2, 3), 16 rows a warp
         {
             const int m = warp & 1;
@@ -311,268 +299,334 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, in
             for (int k = 0; k < DK / 16; ++k) {
                 uint32_t a[4], b[2][4];
                 ldm4(a, &a_rows[16 * m + (lane & 15)][16 * k + (lane >> 4) * 8]);
-                // rows of K are columns of the product: n16 x k16 of two n-tiles
+                // rows of K are columns of the product: two n-tiles
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     ldm4(b[j], &sk[16 * j + (lane & 7) + (lane >> 4) * 8][16 * k + ((lane >> 3) & 1) * 8]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) mma_bf16(acc[j], a, b[j >> 1][2 * (j & 1)], b[j >> 1][2 * (j & 1) + 1]);
             }
+            float(*dst)[kC + 4] = isq ? qk : kk;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = 16 * m + g + 8 * (i >> 1), col = 8 * j + 2 * t + (i & 1);
-                    const float d = expf((s_gh[row] - s_gh[col]) + (s_gl[row] - s_gl[col]));
-                    if (isq) sp[row][col] = col <= row ? acc[j][i] * d * s_rq[row] * s_rk[col] : 0.f;
-                    else sa[row][col] = col < row ? acc[j][i] * d * s_b[row] * s_rk[row] * s_rk[col] : 0.f;
-                }
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<float2*>(&dst[16 * m + g + 8 * i][8 * j + 2 * t]) = make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
         }
         __syncthreads();
-        ChunkData* out = reinterpret_cast<ChunkData*>(p.chunk_ws) + ((size_t)(base + blockIdx.x) * p.H + h);
-        auto put = [&](uint4 (*dst)[2][32], const float (*m)[kC + 4], int tile) {
-            const int r0 = tile ? 16 : 0, c0 = tile == 2 ? 16 : 0;
-            uint32_t hi[4], lo[4];
+        for (int hh = warp >> 1; hh < p.group; hh += 2) {
+            const int h = hq * p.group + hh;
+            ChunkData* out = reinterpret_cast<ChunkData*>(p.chunk_ws) + ((size_t)(base + blockIdx.x) * p.H + h);
+            // decays: a sum in two parts, multiples of 1/8 (exact) and the
+            // rest (small), so that differences of large sums stay exact
+            const size_t at = (size_t)(row0 + min(lane, n_here - 1)) * p.H + h;
+            float gt = lane < n_here ? p.log_decay[at] : 0.f;
+            if (gt < -128.f) gt = -128.f;                        // (-infinity too: e^-128 is 0 in fp32)
+            float gh = rintf(gt * 8.f) * 0.125f, gl = gt - gh;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = *reinterpret_cast<const float2*>(&m[r0 + g + 8 * (i & 1)][c0 + 2 * t + 8 * (i >> 1)]);
-                split2(x.x, x.y, hi[i], lo[i]);
+            for (int o = 1; o < 32; o <<= 1) {
+                const float yh = __shfl_up_sync(0xffffffffu, gh, o), yl = __shfl_up_sync(0xffffffffu, gl, o);
+                if (lane >= o) { gh += yh; gl += yl; }
             }
-            dst[tile][0][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            dst[tile][1][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        };
-        if (warp == 0) {
-            // column `lane` of the inverse, from the top
-            float x[kC];
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                float y[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < i; j += 4) {
-                    const float4 a = *reinterpret_cast<const float4*>(&sa[i][j]);      // (zeros from column i on)
-                    y[0] = fmaf(-a.x, x[j], y[0]);
-                    if (j + 1 < i) y[1] = fmaf(-a.y, x[j + 1], y[1]);
-                    if (j + 2 < i) y[2] = fmaf(-a.z, x[j + 2], y[2]);
-                    if (j + 3 < i) y[3] = fmaf(-a.w, x[j + 3], y[3]);
+            const float b = lane < n_here ? p.beta[at] : 0.f, rk = s_rk[lane];
+            float* xh = s_gh[warp];
+            float* xl = s_gl[warp];
+            __syncwarp();
+            xh[lane] = gh;
+            xl[lane] = gl;
+            __syncwarp();
+            if (!(warp & 1)) {
+                float(*m)[kC + 4] = sa[warp >> 1];
+                const float br = b * rk;
+#pragma unroll 8
+                for (int i = 0; i < kC; ++i) {                   // column `lane` of b_i D_ij (k_i k_j)
+                    const float d = expf((xh[i] - gh) + (xl[i] - gl));
+                    const float bi = __shfl_sync(0xffffffffu, br, i);
+                    m[i][lane] = lane < i ? kk[i][lane] * (bi * rk) * d : 0.f;
                 }
-                x[i] = (y[0] + y[1]) + (y[2] + y[3]);
-            }
-            __syncwarp();
+                __syncwarp();
+                // column `lane` of the inverse, from the top
+                float x[kC];
 #pragma unroll
-            for (int i = 0; i < kC; ++i) sa[i][lane] = x[i];
-            __syncwarp();
-            for (int i = 0; i < 3; ++i) put(out->t, sa, i);
-        } else {
-            put(out->p, sp, warp - 1);
-            if (warp == 1) {
-                const float e = expf(s_gh[lane] + s_gl[lane]), b = s_b[lane];
-                const float w = expf((s_gh[kC - 1] - s_gh[lane]) + (s_gl[kC - 1] - s_gl[lane]));
-                out->f[lane] = make_float4(b, b * e * s_rk[lane], e * s_rq[lane], w * s_rk[lane]);
-                if (lane == kC - 1) out->last = make_float4(e, 0.f, 0.f, 0.f);
+                for (int i = 0; i < kC; ++i) {
+                    float y[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < i; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(&m[i][j]);      // (zeros from column i on)
+                        y[0] = fmaf(-a.x, x[j], y[0]);
+                        if (j + 1 < i) y[1] = fmaf(-a.y, x[j + 1], y[1]);
+                        if (j + 2 < i) y[2] = fmaf(-a.z, x[j + 2], y[2]);
+                        if (j + 3 < i) y[3] = fmaf(-a.w, x[j + 3], y[3]);
+                    }
+                    x[i] = (y[0] + y[1]) + (y[2] + y[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kC; ++i) m[i][lane] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int tile = 0; tile < 6; ++tile) {
+                    const int k = tile >> 2, j = tile < 4 ? tile : tile - 2;
+                    const float2 u0 = *reinterpret_cast<const float2*>(&m[8 * j + g][16 * k + 2 * t]);
+                    const float2 u1 = *reinterpret_cast<const float2*>(&m[8 * j + g][16 * k + 2 * t + 8]);
+                    uint4 w;
+                    split2(u0.x, u0.y, w.x, w.z);
+                    split2(u1.x, u1.y, w.y, w.w);
+                    out->t[tile][lane] = w;
+                }
+            } else {
+                const float e = expf(gh + gl);
+                const float w = expf((xh[kC - 1] - gh) + (xl[kC - 1] - gl));
+                out->b[lane] = b;
+                out->kf[lane] = b * e * rk;
+                out->qf[lane] = e * s_rq[lane];
+                out->wf[lane] = w * rk;
+                if (lane == kC - 1) *reinterpret_cast<float4*>(out->last) = make_float4(e, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int tile = 0; tile < 6; ++tile) {
+                    const int k = tile >> 2, j = tile < 4 ? tile : tile - 2, i = 8 * j + g;
+                    float u[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = 16 * k + 2 * t + (c & 1) + 8 * (c >> 1);
+                        const float d = expf((xh[i] - xh[col]) + (xl[i] - xl[col]));
+                        u[c] = col <= i ? qk[i][col] * (s_rq[i] * s_rk[col]) * d : 0.f;
+                    }
+                    uint4 x;
+                    split2(u[0], u[1], x.x, x.z);
+                    split2(u[2], u[3], x.y, x.w);
+                    out->p[tile][lane] = x;
+                }
             }
         }
     }
 }
 
-constexpr int kScanThreads = 256;
+constexpr int kScanThreads = 128;
 constexpr int kN = 32;                       // state columns of a block
 
 template <int DK>
 struct Scan {
-    uint16_t k[2][kC][DK + 8], q[2][kC][DK + 8];
-    uint16_t s[2][DK][kN + 8];               // the state, high and low terms
-    uint16_t r[2][kC][kN + 8];               // right-hand sides
-    uint16_t u[2][kC][kN + 8];
-    uint16_t w[2][kC][kN + 8];               // exp(G_C - G) |k|^-1 U
+    struct Stage {
+        uint16_t k[kC][DK + 8], q[kC][DK + 8], v[kC][kN + 8];
+        ChunkData d;
+    } st[2];
+    float4 part[4][6][32];                   // a warp's share of K S and Q S for its partner
 };
 
-// Block: kN columns of a head's state.  A warp has a 16 x 8 tile of the
-// chunk's rows (K S and Q S, then U, then out) and 16 rows of the state (or,
-// for head_k 64, half the columns of 16 rows), in fp32 registers from the
-// first chunk to the last.
+// Block: kN columns of a head's state, transposed: with S^T as the first
+// operand a result's registers are the next product's operand as they are.
+// Two warps hold 16 columns, half of the state's rows each, in fp32 registers
+// from the first chunk to the last; they add up their shares of K S and Q S
+// through shared memory, both compute U, and each updates its rows of S and
+// writes half of the tokens.  Tensor-core issue bounds it: about 132 products
+// of 8 cycles a warp and chunk.
 template <int DK>
-__global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, int slots) {
+__global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, int slots) {
     extern __shared__ __align__(16) char smem[];
     Scan<DK>& sm = *reinterpret_cast<Scan<DK>*>(smem);
-    constexpr int MT = DK / 16, NP = 8 / MT, NT = kN / 8 / NP;       // state: row tiles, column parts, 8-column tiles of a part
+    constexpr int KH = DK / 2, NT = KH / 8;                          // state rows of a warp, 8-row tiles
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int gp = warp >> 1, hf = warp & 1;
     const int nb = p.DV / kN;
     const int cb = blockIdx.x % nb, sh = blockIdx.x / nb, s = sh / p.H, h = sh % p.H, hq = h / p.group;
     int base;
     const DeltaRows r = chunk_rows(p, s, slots, &base);
     if (r.n < 0) return;
-    const int m = warp & 1, nt = warp >> 1;                          // tile of the chunk's rows
-    const int sm_row = (warp % MT) * 16, sn = (warp / MT) * NT;      // state rows, first 8-column tile
     const int n_chunks = chunks_of(r.n);
-    const size_t state_at = ((size_t)h * DK + sm_row) * p.DV + cb * kN;
+    // element (column g + 8 i, row 8 j + 2 t + e) of this warp's tile
+    const size_t state_at = ((size_t)h * DK + hf * KH + 2 * t) * p.DV + cb * kN + gp * 16 + g;
     float S[NT][4];
-    {
-        const float* src = r.src >= 0 ? p.states + (size_t)r.src * p.H * DK * p.DV + state_at : nullptr;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[j][i] = 0.f;
+    if (r.src >= 0) {
+        const float* src = p.states + (size_t)r.src * p.H * DK * p.DV + state_at;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 x = src ? *reinterpret_cast<const float2*>(src + (size_t)(g + 8 * i) * p.DV + (sn + j) * 8 + 2 * t)
-                                     : make_float2(0.f, 0.f);
-                S[j][2 * i] = x.x;
-                S[j][2 * i + 1] = x.y;
-            }
+            for (int i = 0; i < 4; ++i) S[j][i] = src[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)];
     }
-    auto store_state = [&]() {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t hi, lo;
-                split2(S[j][2 * i], S[j][2 * i + 1], hi, lo);
-                *reinterpret_cast<uint32_t*>(&sm.s[0][sm_row + g + 8 * i][(sn + j) * 8 + 2 * t]) = hi;
-                *reinterpret_cast<uint32_t*>(&sm.s[1][sm_row + g + 8 * i][(sn + j) * 8 + 2 * t]) = lo;
-            }
-    };
     sm100::grid_dep_wait();                  // the chunks' data is written
     const ChunkData* data = reinterpret_cast<const ChunkData*>(p.chunk_ws) + ((size_t)base * p.H + h);
-    auto load_chunk = [&](int c, int b) {
+    auto load_chunk = [&](int c) {
+        typename Scan<DK>::Stage& x = sm.st[c & 1];
         const int row0 = r.q0 + c * kC, n_here = min(kC, r.n - c * kC);
-        load_rows<DK>(sm.k[b], p.k + (size_t)row0 * p.ks + (size_t)hq * DK, p.ks, n_here, kScanThreads);
-        load_rows<DK>(sm.q[b], p.q + (size_t)row0 * p.qs + (size_t)hq * DK, p.qs, n_here, kScanThreads);
+        load_rows<DK, DK + 8>(&x.k[0][0], p.k + (size_t)row0 * p.ks + (size_t)hq * DK, p.ks, n_here, kScanThreads);
+        load_rows<DK, DK + 8>(&x.q[0][0], p.q + (size_t)row0 * p.qs + (size_t)hq * DK, p.qs, n_here, kScanThreads);
+        load_rows<kN, kN + 8>(&x.v[0][0], p.v + (size_t)row0 * p.vs + (size_t)h * p.DV + cb * kN, p.vs, n_here, kScanThreads);
+        const char* d = reinterpret_cast<const char*>(data + (size_t)c * p.H);
+        for (int i = threadIdx.x; i < (int)(sizeof(ChunkData) / 16); i += kScanThreads)
+            cp_async16(reinterpret_cast<char*>(&x.d) + 16 * i, d + 16 * i);
         cp_async_commit();
     };
-    // a thread's values of a chunk, read a chunk ahead: factors and v of rows
-    // g and g + 8 of its tile, fragments of T and P
-    struct Ahead {
-        float4 f[2];
-        uint32_t v[2];
-        uint4 t[2][2], p[2][2];
-        float last;
+    auto split_a = [&](const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+        split2(x[0], x[1], hi[0], lo[0]);
+        split2(x[2], x[3], hi[1], lo[1]);
+        split2(y[0], y[1], hi[2], lo[2]);
+        split2(y[2], y[3], hi[3], lo[3]);
     };
-    const size_t vcol = (size_t)h * p.DV + cb * kN + nt * 8 + 2 * t;
-    auto fetch = [&](Ahead& a, int c) {
-        const ChunkData* d = data + (size_t)c * p.H;
+    if (n_chunks) load_chunk(0);
+    for (int c = 0; c < n_chunks; ++c) {
+        cp_async_wait<0>();
+        __syncthreads();                     // this chunk is there, and the other stage is read
+        if (c + 1 < n_chunks) load_chunk(c + 1);
+        const typename Scan<DK>::Stage& x = sm.st[c & 1];
+        // ---- this warp's share of (K S)^T and (Q S)^T: 16 columns x 32 tokens
+        float ks[4][4], qs[4][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 16 * m + g + 8 * i;
-            a.f[i] = __ldg(&d->f[row]);
-            // (past the last token: its row, weighed with b = 0)
-            a.v[i] = __ldg(reinterpret_cast<const uint32_t*>(p.v + (size_t)(r.q0 + min(c * kC + row, r.n - 1)) * p.vs + vcol));
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ks[j][i] = qs[j][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KH / 16; ++k) {
+            uint32_t hi[4], lo[4];
+            split_a(S[2 * k], S[2 * k + 1], hi, lo);
+            const int col = hf * KH + 16 * k + ((lane >> 3) & 1) * 8;
+            uint32_t bk[2][4], bq[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ldm4(bk[j], &x.k[16 * j + (lane & 7) + (lane >> 4) * 8][col]);
+                ldm4(bq[j], &x.q[16 * j + (lane & 7) + (lane >> 4) * 8][col]);
+            }
+            // (products that add to the same sums stand far apart here and below)
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mma_bf16(ks[j], o ? lo : hi, bk[j >> 1][2 * (j & 1)], bk[j >> 1][2 * (j & 1) + 1]);
+                    mma_bf16(qs[j], o ? lo : hi, bq[j >> 1][2 * (j & 1)], bq[j >> 1][2 * (j & 1) + 1]);
+                }
+        }
+        // ---- the partner's share: all of K S, and Q S of the tokens this warp writes
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sm.part[warp][j][lane] = make_float4(ks[j][0], ks[j][1], ks[j][2], ks[j][3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 y = hf ? make_float4(qs[j][0], qs[j][1], qs[j][2], qs[j][3])
+                                : make_float4(qs[2 + j][0], qs[2 + j][1], qs[2 + j][2], qs[2 + j][3]);
+            sm.part[warp][4 + j][lane] = y;
+        }
+        sm100::named_bar_sync(1 + gp, 64);
+        float o[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 y = sm.part[warp ^ 1][j][lane];
+            ks[j][0] += y.x;
+            ks[j][1] += y.y;
+            ks[j][2] += y.z;
+            ks[j][3] += y.w;
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)          // (m = 0 has one tile; it reads it twice and uses it once)
+        for (int j = 0; j < 2; ++j) {
+            const float4 y = sm.part[warp ^ 1][4 + j][lane];
+            const float2 f = *reinterpret_cast<const float2*>(&x.d.qf[16 * hf + 8 * j + 2 * t]);
+            o[j][0] = f.x * ((hf ? qs[2 + j][0] : qs[j][0]) + y.x);
+            o[j][1] = f.y * ((hf ? qs[2 + j][1] : qs[j][1]) + y.y);
+            o[j][2] = f.x * ((hf ? qs[2 + j][2] : qs[j][2]) + y.z);
+            o[j][3] = f.y * ((hf ? qs[2 + j][3] : qs[j][3]) + y.w);
+        }
+        // ---- right-hand sides, over K S
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                a.t[k][o] = __ldg(&d->t[m ? 1 + k : 0][o][lane]);
-                a.p[k][o] = __ldg(&d->p[m ? 1 + k : 0][o][lane]);
+        for (int j = 0; j < 2; ++j) {
+            // v^T: columns gp * 16 + g (+ 8), tokens 16 j + 2 t .. and 8 on
+            uint32_t v[4];
+            ldm4t(v, &x.v[16 * j + (lane & 15)][gp * 16 + (lane >> 4) * 8]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 b = *reinterpret_cast<const float2*>(&x.d.b[16 * j + 8 * i + 2 * t]);
+                const float2 f = *reinterpret_cast<const float2*>(&x.d.kf[16 * j + 8 * i + 2 * t]);
+                const float2 v0 = bf16x2_to_f32x2(v[i]), v1 = bf16x2_to_f32x2(v[2 + i]);
+                float(&y)[4] = ks[2 * j + i];
+                y[0] = fmaf(-f.x, y[0], b.x * v0.x);
+                y[1] = fmaf(-f.y, y[1], b.y * v0.y);
+                y[2] = fmaf(-f.x, y[2], b.x * v1.x);
+                y[3] = fmaf(-f.y, y[3], b.y * v1.y);
             }
-        a.last = __ldg(&d->last.x);
-    };
-    // c += M B with M from fragments (high and low), B from two terms in shared memory
-    auto tri = [&](float (&acc)[4], const uint4 (&f)[2][2], const uint16_t (*b)[kC][kN + 8]) {
+        }
+        // ---- U^T
+        float u[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (k > m) continue;
-            uint32_t x[4];                   // k16 x n8: high 0-7, 8-15, low 0-7, 8-15
-            ldm4t(x, &b[lane >> 4][16 * k + (lane & 15)][nt * 8]);
-            const uint32_t hi[4] = {f[k][0].x, f[k][0].y, f[k][0].z, f[k][0].w};
-            const uint32_t lo[4] = {f[k][1].x, f[k][1].y, f[k][1].z, f[k][1].w};
-            mma_bf16(acc, hi, x[0], x[1]);
-            mma_bf16(acc, hi, x[2], x[3]);
-            mma_bf16(acc, lo, x[0], x[1]);
+            uint32_t hi[4], lo[4];
+            split_a(ks[2 * k], ks[2 * k + 1], hi, lo);
+            uint4 f[4];
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) f[j] = x.d.t[k ? j + 2 : j][lane];
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], hi, f[j].x, f[j].y);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], hi, f[j].z, f[j].w);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], lo, f[j].x, f[j].y);
         }
-    };
-    Ahead cur;
-    if (n_chunks) {
-        load_chunk(0, 0);
-        fetch(cur, 0);
-        store_state();
-    }
-    for (int c = 0; c < n_chunks; ++c) {
-        const int b = c & 1;
-        cp_async_wait<0>();
-        __syncthreads();                     // the state and this chunk's rows are there; the other buffer is free
-        Ahead next;
-        const int cn = min(c + 1, n_chunks - 1);
-        if (c + 1 < n_chunks) load_chunk(c + 1, b ^ 1);
-        fetch(next, cn);
-        // ---- K S, Q S
-        float ks[2][4], qs[2][4];            // high, low term of S
-#pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ks[o][i] = qs[o][i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-            uint32_t a[4], aq[4], x[4];
-            ldm4(a, &sm.k[b][16 * m + (lane & 15)][16 * k + (lane >> 4) * 8]);
-            ldm4(aq, &sm.q[b][16 * m + (lane & 15)][16 * k + (lane >> 4) * 8]);
-            ldm4t(x, &sm.s[lane >> 4][16 * k + (lane & 15)][nt * 8]);
-            mma_bf16(ks[0], a, x[0], x[1]);
-            mma_bf16(qs[0], aq, x[0], x[1]);
-            mma_bf16(ks[1], a, x[2], x[3]);
-            mma_bf16(qs[1], aq, x[2], x[3]);
-        }
-        // ---- right-hand sides
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 v = bf16x2_to_f32x2(cur.v[i]);
-            uint32_t hi, lo;
-            split2(fmaf(-cur.f[i].y, ks[0][2 * i] + ks[1][2 * i], cur.f[i].x * v.x),
-                   fmaf(-cur.f[i].y, ks[0][2 * i + 1] + ks[1][2 * i + 1], cur.f[i].x * v.y), hi, lo);
-            *reinterpret_cast<uint32_t*>(&sm.r[0][16 * m + g + 8 * i][nt * 8 + 2 * t]) = hi;
-            *reinterpret_cast<uint32_t*>(&sm.r[1][16 * m + g + 8 * i][nt * 8 + 2 * t]) = lo;
-        }
-        __syncthreads();
-        // ---- U
-        float u[4] = {0.f, 0.f, 0.f, 0.f};
-        tri(u, cur.t, sm.r);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t hi, lo;
-            split2(u[2 * i], u[2 * i + 1], hi, lo);
-            *reinterpret_cast<uint32_t*>(&sm.u[0][16 * m + g + 8 * i][nt * 8 + 2 * t]) = hi;
-            *reinterpret_cast<uint32_t*>(&sm.u[1][16 * m + g + 8 * i][nt * 8 + 2 * t]) = lo;
-            split2(cur.f[i].w * u[2 * i], cur.f[i].w * u[2 * i + 1], hi, lo);
-            *reinterpret_cast<uint32_t*>(&sm.w[0][16 * m + g + 8 * i][nt * 8 + 2 * t]) = hi;
-            *reinterpret_cast<uint32_t*>(&sm.w[1][16 * m + g + 8 * i][nt * 8 + 2 * t]) = lo;
-        }
-        __syncthreads();
-        // ---- the state, and to shared memory for the next chunk
+        // ---- the state
+        const float last = x.d.last[0];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[j][i] *= cur.last;
+            for (int i = 0; i < 4; ++i) S[j][i] *= last;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            uint32_t a[4];                   // K^T: 16 state rows x 16 tokens
-            ldm4t(a, &sm.k[b][16 * k + (lane & 7) + (lane >> 4) * 8][sm_row + ((lane >> 3) & 1) * 8]);
+            float w[2][4];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                uint32_t x[4];
-                ldm4t(x, &sm.w[lane >> 4][16 * k + (lane & 15)][(sn + j) * 8]);
-                mma_bf16(S[j], a, x[0], x[1]);
-                mma_bf16(S[j], a, x[2], x[3]);
+            for (int j = 0; j < 2; ++j) {
+                const float2 f = *reinterpret_cast<const float2*>(&x.d.wf[16 * k + 8 * j + 2 * t]);
+                w[j][0] = f.x * u[2 * k + j][0];
+                w[j][1] = f.y * u[2 * k + j][1];
+                w[j][2] = f.x * u[2 * k + j][2];
+                w[j][3] = f.y * u[2 * k + j][3];
             }
-        }
-        store_state();
-        // ---- out
-        float o[4];
+            uint32_t hi[4], lo[4];
+            split_a(w[0], w[1], hi, lo);
+            uint32_t bk[NT / 2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = cur.f[i >> 1].z * (qs[0][i] + qs[1][i]);
-        tri(o, cur.p, sm.u);
+            for (int j = 0; j < NT / 2; ++j) ldm4t(bk[j], &x.k[16 * k + (lane & 15)][hf * KH + 16 * j + (lane >> 4) * 8]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = c * kC + 16 * m + g + 8 * i;
-            if (row < r.n)
-                *reinterpret_cast<uint32_t*>(p.out + (size_t)(r.q0 + row) * p.H * p.DV + vcol) = pack_bf16(o[2 * i], o[2 * i + 1]);
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) mma_bf16(S[j], o ? lo : hi, bk[j >> 1][2 * (j & 1)], bk[j >> 1][2 * (j & 1) + 1]);
         }
-        cur = next;
+        // ---- out^T of 16 tokens
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k > hf) continue;
+            uint32_t hi[4], lo[4];
+            split_a(u[2 * k], u[2 * k + 1], hi, lo);
+            uint4 f[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) f[j] = x.d.p[k ? 4 + j : 2 * hf + j][lane];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].x, f[j].y);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].z, f[j].w);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) mma_bf16(o[j], lo, f[j].x, f[j].y);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // (token 2 t, 2 t + 1 of column g) -> (columns 2 t, 2 t + 1 of token g)
+                uint32_t y;
+                const uint32_t z = pack_bf16(o[j][2 * i], o[j][2 * i + 1]);
+                asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(z));
+                const int row = c * kC + 16 * hf + 8 * j + g;
+                if (row < r.n)
+                    *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kN + gp * 16 + 8 * i + 2 * t) = y;
+            }
     }
     if (r.dst >= 0 && (r.n > 0 || r.dst != r.src)) {
         float* dst = p.states + (size_t)r.dst * p.H * DK * p.DV + state_at;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<float2*>(dst + (size_t)(g + 8 * i) * p.DV + (sn + j) * 8 + 2 * t) =
-                    make_float2(S[j][2 * i], S[j][2 * i + 1]);
+            for (int i = 0; i < 4; ++i) dst[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)] = S[j][i];
     }
 }
 
@@ -588,7 +642,7 @@ template <int DK>
 cudaError_t run_chunks(const DeltaParams& p, cudaStream_t st) {
     const int slots = chunk_slots(p.n_tokens, p.n_seqs);
     const int z = p.n_seqs < 65535 ? p.n_seqs : 65535;
-    k_delta_chunks<DK><<<dim3(chunks_of(p.max_new), p.H, z), kPrepThreads, 0, st>>>(p, slots);
+    k_delta_chunks<DK><<<dim3(chunks_of(p.max_new), p.H / p.group, z), kPrepThreads, 0, st>>>(p, slots);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = allow_smem<k_delta_scan<DK>>(sizeof(Scan<DK>));
