@@ -134,14 +134,6 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     return r;
 }
 
-// Contiguous bytes (16-byte aligned, a multiple of 16) to shared memory.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // Pairs of fp32 in one instruction.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pack2(float a, float b) {
@@ -229,12 +221,12 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
     uint64_t* sc_free = bars + 20;   // [4] and read
     uint64_t* s_full = bars + 24;    // [NB q + b] scores of a buffer done (commit)
     uint64_t* p_full = bars + 28;    // [NB q + b] probabilities written (4 warps)
-    uint64_t* o_done = bars + 32;    // [q] sums of a query tile updated (commit)
-    uint64_t* q_full = bars + 34;    // [q] query tile written
+    uint64_t* o_done = bars + 32;    // [NB q + b] sums updated from a buffer's probabilities (commit)
     uint64_t* pair = bars + 36;      // [quad] CH: the two warps of a row meet
+    uint64_t* q_full = bars + 45;    // [q] query tile written
     uint64_t* chain = bars + 41;     // [quad] CH: the reference of a key tile is known
     uint64_t* final_bar = bars + 40;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 45);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 47);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -248,13 +240,11 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             mbar_init(&sc_free[i], CH ? 4 : 8);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
             mbar_init(&pair[i], 2);
             mbar_init(&chain[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&o_done[i], 1);
-            mbar_init(&q_full[i], CH ? 8 : 4);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], CH ? 8 : 4);
         mbar_init(final_bar, 1);
         *abort_flag = 0;
         p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -296,6 +286,15 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             __syncwarp();
             if (lane == 0) mbar_arrive(&pair[quad]);
             const bool ok = wait(&pair[quad], met++);
+            return !__any_sync(0xffffffffu, !ok);
+        };
+        // The sums with key tile i (of this query tile) in them.  A wait by
+        // parity is sound while the barrier is at most one phase behind: with a
+        // barrier per score buffer the sums of tile i - NB have to be done,
+        // which the scores that this warp waited for last imply (they were
+        // issued after those sums).
+        auto wait_sums = [&](uint32_t i) {
+            const bool ok = wait(&o_done[NB * q + (i & (NB - 1))], i >> kBufLog2);
             return !__any_sync(0xffffffffu, !ok);
         };
         // 16 bytes of a row of the query tile's place (fp16 queries, later bf16 sums)
@@ -448,8 +447,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     }
                     if (grow && t > w.t0) {              // the sums of the earlier tiles are in tensor memory
                         const float f = was == now ? 1.f : ex2(was - now);
-                        dead = !wait(&o_done[q], cnt - 1);
-                        dead = __any_sync(0xffffffffu, dead);
+                        dead = !wait_sums(cnt - 1);
                         if (dead) break;
                         tc_fence_after();
                         __syncwarp();
@@ -510,8 +508,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     if (dead) break;
                     l = s_l[0][row] + s_l[1][row];
                 }
-                dead = !wait(&o_done[q], cnt - 1);
-                dead = __any_sync(0xffffffffu, dead);
+                dead = !wait_sums(cnt - 1);
                 if (dead) break;
                 tc_fence_after();
                 __syncwarp();
@@ -787,7 +784,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                                     if (!ok) break;
                                     tc_fence_after();
                                     sums(q, b, st, j == 0);
-                                    commit(&o_done[q]);
+                                    commit(&o_done[NB * q + b]);
                                 }
                                 if (NB == 2 && ahead) score(q);
                             }

@@ -241,13 +241,31 @@ __device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, si
     }
 }
 
+// The same by one warp: a lane has a column of pieces.
+template <int W, int STRIDE>
+__device__ __forceinline__ void rows_async(uint16_t* dst, const uint16_t* src, size_t stride, int n_here, int lane) {
+    constexpr int PC = W / 8, RP = 32 / PC;      // pieces of a row, rows of a pass
+    const int row = lane / PC, c = lane % PC * 8;
+    dst += row * STRIDE + c;
+    src += row * stride + c;
+    if (n_here == kC) {
+#pragma unroll
+        for (int i = 0; i < kC / RP; ++i) cp_async16(dst + i * RP * STRIDE, src + i * RP * stride);
+    } else {
+        for (int i = 0; i < kC / RP; ++i) {
+            if (row + i * RP < n_here) cp_async16(dst + i * RP * STRIDE, src + i * RP * stride);
+            else *reinterpret_cast<uint4*>(dst + i * RP * STRIDE) = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 constexpr int kPrepThreads = 128;
 
 // Block (chunk, head of q and k, sequence).  K K^T and Q K^T once, then two of
 // the heads that share them at a time, two warps each: one for T, one for P
 // and the factors.
 template <int DK>
-__global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, int slots) {
+__global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p, int slots) {
     __shared__ __align__(16) uint16_t sk[kC][DK + 8], sq[kC][DK + 8];
     __shared__ __align__(16) float kk[kC][kC + 4], qk[kC][kC + 4], sa[2][kC][kC + 4];
     __shared__ float s_rk[kC], s_rq[kC], s_gh[4][kC], s_gl[4][kC];
@@ -345,25 +363,63 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, in
                     m[i][lane] = lane < i ? kk[i][lane] * (bi * rk) * d : 0.f;
                 }
                 __syncwarp();
-                // column `lane` of the inverse, from the top
-                float x[kC];
+                // the inverse by blocks of 16: T11 and T22 a column a lane,
+                // from the top, then T21 = -T22 A21 T11
+                {
+                    const int o = lane & 16, cj = lane & 15;
+                    float x[16];
 #pragma unroll
-                for (int i = 0; i < kC; ++i) {
-                    float y[4] = {i == lane ? 1.f : 0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < 16; ++i) {
+                        float y[4] = {i == cj ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int j = 0; j < i; j += 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(&m[i][j]);      // (zeros from column i on)
-                        y[0] = fmaf(-a.x, x[j], y[0]);
-                        if (j + 1 < i) y[1] = fmaf(-a.y, x[j + 1], y[1]);
-                        if (j + 2 < i) y[2] = fmaf(-a.z, x[j + 2], y[2]);
-                        if (j + 3 < i) y[3] = fmaf(-a.w, x[j + 3], y[3]);
+                        for (int j = 0; j < i; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(&m[o + i][o + j]);   // (zeros from column i on)
+                            y[0] = fmaf(-a.x, x[j], y[0]);
+                            if (j + 1 < i) y[1] = fmaf(-a.y, x[j + 1], y[1]);
+                            if (j + 2 < i) y[2] = fmaf(-a.z, x[j + 2], y[2]);
+                            if (j + 3 < i) y[3] = fmaf(-a.w, x[j + 3], y[3]);
+                        }
+                        x[i] = (y[0] + y[1]) + (y[2] + y[3]);
                     }
-                    x[i] = (y[0] + y[1]) + (y[2] + y[3]);
-                }
-                __syncwarp();
+                    __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kC; ++i) m[i][lane] = x[i];
-                __syncwarp();
+                    for (int i = 0; i < 16; ++i) m[o + i][lane] = x[i];
+                    __syncwarp();
+                    // (A21 T11 stands in the upper right block, which no tile holds)
+                    const int rb = o >> 1;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = m[i][cj];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(&m[16 + rb + i][j]);
+                            y[0] = fmaf(a.x, x[j], y[0]);
+                            y[1] = fmaf(a.y, x[j + 1], y[1]);
+                            y[2] = fmaf(a.z, x[j + 2], y[2]);
+                            y[3] = fmaf(a.w, x[j + 3], y[3]);
+                        }
+                        m[rb + i][16 + cj] = (y[0] + y[1]) + (y[2] + y[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = m[i][16 + cj];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 a = *reinterpret_cast<const float4*>(&m[16 + rb + i][16 + j]);
+                            y[0] = fmaf(-a.x, x[j], y[0]);
+                            y[1] = fmaf(-a.y, x[j + 1], y[1]);
+                            y[2] = fmaf(-a.z, x[j + 2], y[2]);
+                            y[3] = fmaf(-a.w, x[j + 3], y[3]);
+                        }
+                        m[16 + rb + i][cj] = (y[0] + y[1]) + (y[2] + y[3]);
+                    }
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int tile = 0; tile < 6; ++tile) {
                     const int k = tile >> 2, j = tile < 4 ? tile : tile - 2;
@@ -402,7 +458,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_chunks(DeltaParams p, in
     }
 }
 
-constexpr int kScanThreads = 128;
+constexpr int kScanThreads = 160;           // four warps compute, the fifth loads
+constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 constexpr int kN = 32;                       // state columns of a block
 
 template <int DK>
@@ -412,6 +469,9 @@ struct Scan {
         ChunkData d;
     } st[2];
     float4 part[4][6][32];                   // a warp's share of K S and Q S for its partner
+    uint64_t full[2], empty[2];              // stages
+    uint64_t wrote[2], read[2];              // shares of the two warps of a group
+    int abort;
 };
 
 // Block: kN columns of a head's state, transposed: with S^T as the first
@@ -419,10 +479,11 @@ struct Scan {
 // Two warps hold 16 columns, half of the state's rows each, in fp32 registers
 // from the first chunk to the last; they add up their shares of K S and Q S
 // through shared memory, both compute U, and each updates its rows of S and
-// writes half of the tokens.  Tensor-core issue bounds it: about 132 products
-// of 8 cycles a warp and chunk.
+// writes half of the tokens.  The chain of a chunk's steps bounds it (about
+// 3000 cycles of latencies; its 132 products take 8 cycles each), so all that
+// is not on it is done by the fifth warp, which keeps a chunk ahead.
 template <int DK>
-__global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, int slots) {
+__global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, int slots) {
     extern __shared__ __align__(16) char smem[];
     Scan<DK>& sm = *reinterpret_cast<Scan<DK>*>(smem);
     constexpr int KH = DK / 2, NT = KH / 8;                          // state rows of a warp, 8-row tiles
@@ -434,6 +495,42 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
     const DeltaRows r = chunk_rows(p, s, slots, &base);
     if (r.n < 0) return;
     const int n_chunks = chunks_of(r.n);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            sm100::mbar_init(&sm.full[i], 32);
+            sm100::mbar_init(&sm.empty[i], 4);
+            sm100::mbar_init(&sm.wrote[i], 2);
+            sm100::mbar_init(&sm.read[i], 2);
+        }
+        sm.abort = 0;
+        sm100::fence_barrier_init();
+    }
+    __syncthreads();
+    volatile int* abort = &sm.abort;
+    if (warp == 4) {
+        sm100::grid_dep_wait();              // the chunks' data is written
+        const ChunkData* data = reinterpret_cast<const ChunkData*>(p.chunk_ws) + ((size_t)base * p.H + h);
+        int c = 0;
+        for (; c < n_chunks; ++c) {
+            const bool ok = sm100::mbar_wait(&sm.empty[c & 1], ((c >> 1) & 1) ^ 1, abort, kWaitLimit);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            typename Scan<DK>::Stage& x = sm.st[c & 1];
+            const int n_here = min(kC, r.n - c * kC);
+            const size_t row0 = (size_t)r.q0 + (size_t)c * kC;
+            rows_async<DK, DK + 8>(&x.k[0][0], p.k + row0 * p.ks + (size_t)hq * DK, p.ks, n_here, lane);
+            rows_async<DK, DK + 8>(&x.q[0][0], p.q + row0 * p.qs + (size_t)hq * DK, p.qs, n_here, lane);
+            rows_async<kN, kN + 8>(&x.v[0][0], p.v + row0 * p.vs + (size_t)h * p.DV + cb * kN, p.vs, n_here, lane);
+            const char* d = reinterpret_cast<const char*>(data + (size_t)c * p.H) + 16 * lane;
+            char* xd = reinterpret_cast<char*>(&x.d) + 16 * lane;
+            constexpr int kWhole = sizeof(ChunkData) / 512;
+#pragma unroll
+            for (int i = 0; i < kWhole; ++i) cp_async16(xd + 512 * i, d + 512 * i);
+            if (lane < (int)(sizeof(ChunkData) % 512 / 16)) cp_async16(xd + 512 * kWhole, d + 512 * kWhole);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(&sm.full[c & 1])) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        return;
+    }
     // element (column g + 8 i, row 8 j + 2 t + e) of this warp's tile
     const size_t state_at = ((size_t)h * DK + hf * KH + 2 * t) * p.DV + cb * kN + gp * 16 + g;
     float S[NT][4];
@@ -448,30 +545,17 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j][i] = src[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)];
     }
-    sm100::grid_dep_wait();                  // the chunks' data is written
-    const ChunkData* data = reinterpret_cast<const ChunkData*>(p.chunk_ws) + ((size_t)base * p.H + h);
-    auto load_chunk = [&](int c) {
-        typename Scan<DK>::Stage& x = sm.st[c & 1];
-        const int row0 = r.q0 + c * kC, n_here = min(kC, r.n - c * kC);
-        load_rows<DK, DK + 8>(&x.k[0][0], p.k + (size_t)row0 * p.ks + (size_t)hq * DK, p.ks, n_here, kScanThreads);
-        load_rows<DK, DK + 8>(&x.q[0][0], p.q + (size_t)row0 * p.qs + (size_t)hq * DK, p.qs, n_here, kScanThreads);
-        load_rows<kN, kN + 8>(&x.v[0][0], p.v + (size_t)row0 * p.vs + (size_t)h * p.DV + cb * kN, p.vs, n_here, kScanThreads);
-        const char* d = reinterpret_cast<const char*>(data + (size_t)c * p.H);
-        for (int i = threadIdx.x; i < (int)(sizeof(ChunkData) / 16); i += kScanThreads)
-            cp_async16(reinterpret_cast<char*>(&x.d) + 16 * i, d + 16 * i);
-        cp_async_commit();
-    };
     auto split_a = [&](const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
         split2(x[0], x[1], hi[0], lo[0]);
         split2(x[2], x[3], hi[1], lo[1]);
         split2(y[0], y[1], hi[2], lo[2]);
         split2(y[2], y[3], hi[3], lo[3]);
     };
-    if (n_chunks) load_chunk(0);
+    bool dead = false;
     for (int c = 0; c < n_chunks; ++c) {
-        cp_async_wait<0>();
-        __syncthreads();                     // this chunk is there, and the other stage is read
-        if (c + 1 < n_chunks) load_chunk(c + 1);
+        dead = !sm100::mbar_wait(&sm.full[c & 1], (c >> 1) & 1, abort, kWaitLimit);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
         const typename Scan<DK>::Stage& x = sm.st[c & 1];
         // ---- this warp's share of (K S)^T and (Q S)^T: 16 columns x 32 tokens
         float ks[4][4], qs[4][4];
@@ -500,6 +584,9 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
                 }
         }
         // ---- the partner's share: all of K S, and Q S of the tokens this warp writes
+        dead = c > 0 && !sm100::mbar_wait(&sm.read[gp], (c - 1) & 1, abort, kWaitLimit);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) sm.part[warp][j][lane] = make_float4(ks[j][0], ks[j][1], ks[j][2], ks[j][3]);
 #pragma unroll
@@ -508,7 +595,18 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
                                 : make_float4(qs[2 + j][0], qs[2 + j][1], qs[2 + j][2], qs[2 + j][3]);
             sm.part[warp][4 + j][lane] = y;
         }
-        sm100::named_bar_sync(1 + gp, 64);
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sm.wrote[gp]);
+        // (what the next steps read, while the partner's share is on its way)
+        uint32_t v[2][4];
+        uint4 ft[6];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) ldm4t(v[j], &x.v[16 * j + (lane & 15)][gp * 16 + (lane >> 4) * 8]);
+#pragma unroll
+        for (int j = 0; j < 6; ++j) ft[j] = x.d.t[j][lane];
+        dead = !sm100::mbar_wait(&sm.wrote[gp], c & 1, abort, kWaitLimit);
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) break;
         float o[2][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -527,17 +625,17 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
             o[j][2] = f.x * ((hf ? qs[2 + j][2] : qs[j][2]) + y.z);
             o[j][3] = f.y * ((hf ? qs[2 + j][3] : qs[j][3]) + y.w);
         }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sm.read[gp]);
         // ---- right-hand sides, over K S
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             // v^T: columns gp * 16 + g (+ 8), tokens 16 j + 2 t .. and 8 on
-            uint32_t v[4];
-            ldm4t(v, &x.v[16 * j + (lane & 15)][gp * 16 + (lane >> 4) * 8]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 b = *reinterpret_cast<const float2*>(&x.d.b[16 * j + 8 * i + 2 * t]);
                 const float2 f = *reinterpret_cast<const float2*>(&x.d.kf[16 * j + 8 * i + 2 * t]);
-                const float2 v0 = bf16x2_to_f32x2(v[i]), v1 = bf16x2_to_f32x2(v[2 + i]);
+                const float2 v0 = bf16x2_to_f32x2(v[j][i]), v1 = bf16x2_to_f32x2(v[j][2 + i]);
                 float(&y)[4] = ks[2 * j + i];
                 y[0] = fmaf(-f.x, y[0], b.x * v0.x);
                 y[1] = fmaf(-f.y, y[1], b.y * v0.y);
@@ -555,9 +653,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
         for (int k = 0; k < 2; ++k) {
             uint32_t hi[4], lo[4];
             split_a(ks[2 * k], ks[2 * k + 1], hi, lo);
-            uint4 f[4];
-#pragma unroll
-            for (int j = 2 * k; j < 4; ++j) f[j] = x.d.t[k ? j + 2 : j][lane];
+            const uint4* f = ft + 2 * k;
 #pragma unroll
             for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], hi, f[j].x, f[j].y);
 #pragma unroll
@@ -608,6 +704,8 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int j = 0; j < 2; ++j) mma_bf16(o[j], lo, f[j].x, f[j].y);
         }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sm.empty[c & 1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -620,6 +718,10 @@ __global__ void __launch_bounds__(kScanThreads, 3) k_delta_scan(DeltaParams p, i
                 if (row < r.n)
                     *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kN + gp * 16 + 8 * i + 2 * t) = y;
             }
+    }
+    if (dead) {
+        if (lane == 0) set_status(p.ctrl, LMOE_ERR_TIMEOUT);
+        return;
     }
     if (r.dst >= 0 && (r.n > 0 || r.dst != r.src)) {
         float* dst = p.states + (size_t)r.dst * p.H * DK * p.DV + state_at;
