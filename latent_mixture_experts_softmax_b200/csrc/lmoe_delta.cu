@@ -261,6 +261,14 @@ __device__ __forceinline__ void rows_async(uint16_t* dst, const uint16_t* src, s
 
 constexpr int kPrepThreads = 128;
 
+// e^x for x <= 0.  The product is rounded by |x| 2^-24, which moves e^x by less
+// than 2^-25 in all.
+__device__ __forceinline__ float exp_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
 // Block (chunk, head of q and k, sequence).  K K^T and Q K^T once, then two of
 // the heads that share them at a time, two warps each: one for T, one for P
 // and the factors.
@@ -282,26 +290,20 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
         cp_async_commit();
         cp_async_wait<0>();
         __syncthreads();
-        // norms: four threads a row
+        // norms of q, four threads a row (those of k are the diagonal of K K^T)
         {
             const int row = threadIdx.x >> 2;
-            float nk = 0.f, nq = 0.f;
+            float nq = 0.f;
+            if (p.l2norm) {
 #pragma unroll
-            for (int i = 0; i < DK / 8; ++i) {
-                const float2 a = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sk[row][2 * (t + 4 * i)]));
-                const float2 b = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sq[row][2 * (t + 4 * i)]));
-                nk = fmaf(a.x, a.x, fmaf(a.y, a.y, nk));
-                nq = fmaf(b.x, b.x, fmaf(b.y, b.y, nq));
-            }
+                for (int i = 0; i < DK / 8; ++i) {
+                    const float2 b = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sq[row][2 * (t + 4 * i)]));
+                    nq = fmaf(b.x, b.x, fmaf(b.y, b.y, nq));
+                }
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                nk += __shfl_xor_sync(0xffffffffu, nk, o);
-                nq += __shfl_xor_sync(0xffffffffu, nq, o);
+                for (int o = 1; o < 4; o <<= 1) nq += __shfl_xor_sync(0xffffffffu, nq, o);
             }
-            if (t == 0) {
-                s_rk[row] = p.l2norm ? 1.f / sqrtf(nk + 1e-6f) : 1.f;
-                s_rq[row] = p.scale * (p.l2norm ? 1.f / sqrtf(nq + 1e-6f) : 1.f);
-            }
+            if (t == 0) s_rq[row] = p.scale * (p.l2norm ? 1.f / sqrtf(nq + 1e-6f) : 1.f);
         }
         // K K^T (warps 0, 1) and Q K^T (2, 3), 16 rows a warp
         {
@@ -332,6 +334,9 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                     *reinterpret_cast<float2*>(&dst[16 * m + g + 8 * i][8 * j + 2 * t]) = make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
         }
         __syncthreads();
+        const float rk = p.l2norm ? 1.f / sqrtf(kk[lane][lane] + 1e-6f) : 1.f;
+        if (warp == 0) s_rk[lane] = rk;
+        __syncthreads();
         for (int hh = warp >> 1; hh < p.group; hh += 2) {
             const int h = hq * p.group + hh;
             ChunkData* out = reinterpret_cast<ChunkData*>(p.chunk_ws) + ((size_t)(base + blockIdx.x) * p.H + h);
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                 const float yh = __shfl_up_sync(0xffffffffu, gh, o), yl = __shfl_up_sync(0xffffffffu, gl, o);
                 if (lane >= o) { gh += yh; gl += yl; }
             }
-            const float b = lane < n_here ? p.beta[at] : 0.f, rk = s_rk[lane];
+            const float b = lane < n_here ? p.beta[at] : 0.f;
             float* xh = s_gh[warp];
             float* xl = s_gl[warp];
             __syncwarp();
@@ -358,7 +363,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                 const float br = b * rk;
 #pragma unroll 8
                 for (int i = 0; i < kC; ++i) {                   // column `lane` of b_i D_ij (k_i k_j)
-                    const float d = expf((xh[i] - gh) + (xl[i] - gl));
+                    const float d = exp_of((xh[i] - gh) + (xl[i] - gl));
                     const float bi = __shfl_sync(0xffffffffu, br, i);
                     m[i][lane] = lane < i ? kk[i][lane] * (bi * rk) * d : 0.f;
                 }
@@ -431,8 +436,8 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                     out->t[tile][lane] = w;
                 }
             } else {
-                const float e = expf(gh + gl);
-                const float w = expf((xh[kC - 1] - gh) + (xl[kC - 1] - gl));
+                const float e = exp_of(gh + gl);
+                const float w = exp_of((xh[kC - 1] - gh) + (xl[kC - 1] - gl));
                 out->b[lane] = b;
                 out->kf[lane] = b * e * rk;
                 out->qf[lane] = e * s_rq[lane];
@@ -445,7 +450,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int col = 16 * k + 2 * t + (c & 1) + 8 * (c >> 1);
-                        const float d = expf((xh[i] - xh[col]) + (xl[i] - xl[col]));
+                        const float d = exp_of((xh[i] - xh[col]) + (xl[i] - xl[col]));
                         u[c] = col <= i ? qk[i][col] * (s_rq[i] * s_rk[col]) * d : 0.f;
                     }
                     uint4 x;
