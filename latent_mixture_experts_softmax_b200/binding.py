@@ -163,7 +163,7 @@ def _ptr(a):
 
 
 def _nbytes(a):
-    return a.numel() * a.element_size()
+    return a.nbytes
 
 
 def _stream(stream):

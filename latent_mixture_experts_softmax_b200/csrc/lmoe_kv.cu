@@ -3,9 +3,12 @@
 //
 // Both kernels are copies with a little arithmetic, bound by HBM: a write
 // reads 2 bytes an element and stores 1 (and 4 a row), a read the reverse.
-// A row's D elements are spread over D / 8 lanes, 16 bytes of bf16 each, so
-// a row's maximum is a few shuffles and every access of a warp is whole
-// 32-byte sectors.
+// A block takes some tokens, looks up their places once (a search, the
+// sequence's lengths and its page: four loads one behind the other, which a
+// thread per row paid for every 16 bytes), and then moves their rows, four
+// 8-element pieces in flight per thread.  A row's D elements are spread over
+// D / 8 lanes, 16 bytes of bf16 each, so a row's maximum is a few shuffles and
+// every access of a warp is whole 32-byte sectors.
 
 #include "lmoe_mixers.cuh"
 
@@ -50,116 +53,164 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
     return r;
 }
 
-// One row of D elements per D / 8 lanes; grid.y: 0 keys, 1 values.
+constexpr int kPieces = 4;        // pieces in flight per thread
+constexpr int kMaxTokens = 64;    // tokens of a block
+
+// Places of the block's tokens.
+__device__ __forceinline__ void find_places(const KvParams& p, long long (&place)[kMaxTokens], int tok0, int n) {
+    if ((int)threadIdx.x < n) place[threadIdx.x] = place_of_row(p, tok0 + threadIdx.x);
+    __syncthreads();
+}
+
+// grid.x: runs of `tokens` tokens; grid.y: 0 keys, 1 values.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_append(KvParams p, const uint16_t* __restrict__ kx,
                                                         const uint16_t* __restrict__ vx, size_t k_stride,
-                                                        size_t v_stride) {
+                                                        size_t v_stride, int tokens) {
     constexpr int LANES = D / 8;
-    const int lane = threadIdx.x % LANES;
-    const size_t item = (size_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    const int tok = (int)(item / p.Hk), head = (int)(item % p.Hk);
+    __shared__ long long s_place[kMaxTokens];
     const bool is_v = blockIdx.y == 1;
-    const long long place = tok < p.n_tokens ? place_of_row(p, tok) : -1;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (place >= 0) {
-        const uint16_t* src = is_v ? vx + (size_t)tok * v_stride : kx + (size_t)tok * k_stride;
-        w = ldg_stream(reinterpret_cast<const uint4*>(src + (size_t)head * D + lane * 8));
-    }
-    // max |x| as bf16 bits (their order is that of the magnitudes, NaN last)
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t m = 0;
+    const int tok0 = blockIdx.x * tokens, n = min(tokens, p.n_tokens - tok0);
+    find_places(p, s_place, tok0, n);
+    const uint16_t* src = is_v ? vx : kx;
+    const size_t stride = is_v ? v_stride : k_stride;
+    uint8_t* codes = is_v ? p.v : p.k;
+    float* scales = is_v ? p.vs : p.ks;
+    const int total = n * p.Hk * LANES, lane = threadIdx.x % LANES;
+    for (int base = 0; base < total; base += kThreads * kPieces) {
+        uint4 w[kPieces];
+        long long row[kPieces];                // the row in the scale arrays, -1: none
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (place < 0) return;
-    float a = bf16_bits_to_f32(m);
-    constexpr float kTop = FMT == LMOE_KV_INT8 ? 127.f : 448.f;
-    float scale = __fdiv_rn(a, kTop);
-    uint32_t c[2] = {0, 0};
-    if (m >= 0x7f80u) {                       // infinity or NaN
-        scale = __int_as_float(0x7fffffff);
-        set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
-    } else if (a < 0x1p-100f) {
-        scale = 1.f;
-    } else {
-        // code = round(top * x / a).  top * x is exact (8 + 7 bits), so the
-        // correctly rounded quotient decides as exact arithmetic does: a
-        // quotient that is no tie is at least 2^-9 of a step away from one.
-        // Rows beyond 2^64 are scaled down by a power of two first, so that
-        // the product stays finite.
-        const float f = a > 0x1p64f ? 0x1p-64f : 1.f;
-        a *= f;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = bf16x2_to_f32x2(u[i]);
-            y[2 * i] = __fdiv_rn(x.x * f * kTop, a);
-            y[2 * i + 1] = __fdiv_rn(x.y * f * kTop, a);
+        for (int i = 0; i < kPieces; ++i) {
+            // (every load has a place to read, so that none waits for a condition)
+            const int r = min(base + i * kThreads + (int)threadIdx.x, total - LANES + lane) / LANES;
+            const int tok = r / p.Hk, head = r - tok * p.Hk;
+            const long long place = s_place[tok];
+            row[i] = place >= 0 && base + i * kThreads + (int)threadIdx.x < total
+                         ? place + ((long long)head << p.page_log2) : -1;
+            w[i] = ldg_stream(reinterpret_cast<const uint4*>(src + (size_t)(tok0 + tok) * stride + (size_t)head * D + lane * 8));
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (FMT == LMOE_KV_INT8) {
+        for (int i = 0; i < kPieces; ++i) {
+            // max |x| as bf16 bits (their order is that of the magnitudes, NaN last)
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) c[i] |= (uint32_t)(__float2int_rn(y[4 * i + j]) & 0xff) << (8 * j);
+            for (int j = 0; j < 4; ++j) m = max(m, max(u[j] & 0x7fffu, (u[j] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (row[i] < 0) continue;
+            float a = bf16_bits_to_f32(m);
+            constexpr float kTop = FMT == LMOE_KV_INT8 ? 127.f : 448.f;
+            float scale = __fdiv_rn(a, kTop);
+            uint32_t c[2] = {0, 0};
+            if (m >= 0x7f80u) {                       // infinity or NaN
+                scale = __int_as_float(0x7fffffff);
+                set_status(p.ctrl, LMOE_ERR_DEVICE_CHECK);
+            } else if (a < 0x1p-100f) {
+                scale = 1.f;
             } else {
-                c[i] = e4m3x2_of(y[4 * i], y[4 * i + 1]) | e4m3x2_of(y[4 * i + 2], y[4 * i + 3]) << 16;
+                // code = round(top * x / a).  top * x is exact (8 + 7 bits), so the
+                // correctly rounded quotient decides as exact arithmetic does: a
+                // quotient that is no tie is at least 2^-9 of a step away from one.
+                // Rows beyond 2^64 are scaled down by a power of two first, so that
+                // the product stays finite.
+                const float f = a > 0x1p64f ? 0x1p-64f : 1.f;
+                a *= f;
+                float y[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = bf16x2_to_f32x2(u[j]);
+                    y[2 * j] = __fdiv_rn(x.x * f * kTop, a);
+                    y[2 * j + 1] = __fdiv_rn(x.y * f * kTop, a);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (FMT == LMOE_KV_INT8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[j] |= (uint32_t)(__float2int_rn(y[4 * j + e]) & 0xff) << (8 * e);
+                    } else {
+                        c[j] = e4m3x2_of(y[4 * j], y[4 * j + 1]) | e4m3x2_of(y[4 * j + 2], y[4 * j + 3]) << 16;
+                    }
+                }
             }
+            *reinterpret_cast<uint2*>(codes + row[i] * D + lane * 8) = make_uint2(c[0], c[1]);
+            if (lane == 0) scales[row[i]] = scale;
         }
     }
-    const size_t row = (size_t)place + ((size_t)head << p.page_log2);
-    *reinterpret_cast<uint2*>((is_v ? p.v : p.k) + row * D + lane * 8) = make_uint2(c[0], c[1]);
-    if (lane == 0) (is_v ? p.vs : p.ks)[row] = scale;
 }
 
-// One row per D / 8 lanes, as above.
+// The same grid.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) k_kv_read(KvParams p, uint16_t* __restrict__ ky, uint16_t* __restrict__ vy,
-                                                      size_t k_stride, size_t v_stride) {
+                                                      size_t k_stride, size_t v_stride, int tokens) {
     constexpr int LANES = D / 8;
-    const int lane = threadIdx.x % LANES;
-    const size_t item = (size_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-    const int tok = (int)(item / p.Hk), head = (int)(item % p.Hk);
+    __shared__ long long s_place[kMaxTokens];
     const bool is_v = blockIdx.y == 1;
-    if (tok >= p.n_tokens) return;
-    const long long place = place_of_row(p, tok);
-    if (place == -1) return;
-    uint32_t o[4] = {0, 0, 0, 0};
-    if (place >= 0) {
-        const size_t row = (size_t)place + ((size_t)head << p.page_log2);
-        const float scale = __ldg((is_v ? p.vs : p.ks) + row);
-        const uint2 c = __ldg(reinterpret_cast<const uint2*>((is_v ? p.v : p.k) + row * D + lane * 8));
-        float y[8];
-        if (FMT == LMOE_KV_INT8) {
+    const int tok0 = blockIdx.x * tokens, n = min(tokens, p.n_tokens - tok0);
+    find_places(p, s_place, tok0, n);
+    uint16_t* dst = is_v ? vy : ky;
+    const size_t stride = is_v ? v_stride : k_stride;
+    const uint8_t* codes = is_v ? p.v : p.k;
+    const float* scales = is_v ? p.vs : p.ks;
+    const int total = n * p.Hk * LANES, lane = threadIdx.x % LANES;
+    for (int base = 0; base < total; base += kThreads * kPieces) {
+        uint2 c[kPieces];
+        float scale[kPieces];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = (float)(int8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
-        } else {
-            float lo[4], hi[4];
-            e4m3x4_to_f32x4(c.x, lo);
-            e4m3x4_to_f32x4(c.y, hi);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { y[i] = lo[i]; y[4 + i] = hi[i]; }
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = min(base + i * kThreads + (int)threadIdx.x, total - LANES + lane) / LANES;
+            const int tok = r / p.Hk, head = r - tok * p.Hk;
+            const long long place = s_place[tok];      // (without one: row 0 is read and dropped)
+            const size_t row = place >= 0 ? (size_t)place + ((size_t)head << p.page_log2) : 0;
+            scale[i] = __ldg(scales + row);
+            c[i] = __ldg(reinterpret_cast<const uint2*>(codes + row * D + lane * 8));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = (uint32_t)f32_to_bf16_bits(y[2 * i] * scale) | (uint32_t)f32_to_bf16_bits(y[2 * i + 1] * scale) << 16;
+        for (int i = 0; i < kPieces; ++i) {
+            const int idx = base + i * kThreads + (int)threadIdx.x;
+            if (idx >= total) continue;
+            const int r = idx / LANES, tok = r / p.Hk, head = r - tok * p.Hk;
+            const long long place = s_place[tok];
+            if (place == -1) continue;
+            uint32_t o[4] = {0, 0, 0, 0};
+            if (place >= 0) {
+                float y[8];
+                if (FMT == LMOE_KV_INT8) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = (float)(int8_t)((j < 4 ? c[i].x : c[i].y) >> (8 * (j & 3)));
+                } else {
+                    float lo[4], hi[4];
+                    e4m3x4_to_f32x4(c[i].x, lo);
+                    e4m3x4_to_f32x4(c[i].y, hi);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) { y[j] = lo[j]; y[4 + j] = hi[j]; }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(y[2 * j + 1] * scale[i]), "f"(y[2 * j] * scale[i]));
+            }
+            *reinterpret_cast<uint4*>(dst + (size_t)(tok0 + tok) * stride + (size_t)head * D + lane * 8) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
-    uint16_t* dst = is_v ? vy + (size_t)tok * v_stride : ky + (size_t)tok * k_stride;
-    *reinterpret_cast<uint4*>(dst + (size_t)head * D + lane * 8) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-dim3 row_grid(const KvParams& p) {
-    const size_t rows = (size_t)p.n_tokens * p.Hk, per = kThreads / (p.D / 8);
-    return dim3((unsigned)((rows + per - 1) / per), 2);
+// Tokens of a block: two rounds of pieces, or fewer where the tokens are too
+// few to fill the SMs with that.
+int block_tokens(const KvParams& p) {
+    const int fill = 2 * kThreads * kPieces / (p.Hk * (p.D / 8)), spread = (p.n_tokens + kSms - 1) / kSms;
+    const int n = fill < spread ? fill : spread;
+    return n < 1 ? 1 : n > kMaxTokens ? kMaxTokens : n;
 }
 
 }  // namespace
 
 cudaError_t run_kv_append(const KvParams& p, const uint16_t* k, const uint16_t* v, size_t k_stride, size_t v_stride,
                           cudaStream_t st) {
-    const dim3 g = row_grid(p);
-    auto go = [&](auto kernel) { kernel<<<g, kThreads, 0, st>>>(p, k, v, k_stride, v_stride); };
+    const int tokens = block_tokens(p);
+    const dim3 g((unsigned)((p.n_tokens + tokens - 1) / tokens), 2);
+    auto go = [&](auto kernel) { kernel<<<g, kThreads, 0, st>>>(p, k, v, k_stride, v_stride, tokens); };
     const bool i8 = p.fmt == LMOE_KV_INT8;
     if (p.D == 64) i8 ? go(k_kv_append<64, LMOE_KV_INT8>) : go(k_kv_append<64, LMOE_KV_E4M3>);
     else if (p.D == 128) i8 ? go(k_kv_append<128, LMOE_KV_INT8>) : go(k_kv_append<128, LMOE_KV_E4M3>);
@@ -169,8 +220,9 @@ cudaError_t run_kv_append(const KvParams& p, const uint16_t* k, const uint16_t* 
 
 cudaError_t run_kv_read(const KvParams& p, uint16_t* k, uint16_t* v, size_t k_stride, size_t v_stride,
                         cudaStream_t st) {
-    const dim3 g = row_grid(p);
-    auto go = [&](auto kernel) { kernel<<<g, kThreads, 0, st>>>(p, k, v, k_stride, v_stride); };
+    const int tokens = block_tokens(p);
+    const dim3 g((unsigned)((p.n_tokens + tokens - 1) / tokens), 2);
+    auto go = [&](auto kernel) { kernel<<<g, kThreads, 0, st>>>(p, k, v, k_stride, v_stride, tokens); };
     const bool i8 = p.fmt == LMOE_KV_INT8;
     if (p.D == 64) i8 ? go(k_kv_read<64, LMOE_KV_INT8>) : go(k_kv_read<64, LMOE_KV_E4M3>);
     else if (p.D == 128) i8 ? go(k_kv_read<128, LMOE_KV_INT8>) : go(k_kv_read<128, LMOE_KV_E4M3>);

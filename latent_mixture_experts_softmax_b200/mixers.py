@@ -26,25 +26,20 @@ _KV = {"int8": (B.LMOE_KV_INT8, torch.int8), "e4m3": (B.LMOE_KV_E4M3, torch.floa
 
 
 def _stream_of(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+    # (the raw handle: torch.cuda.current_stream builds an object, a third of a small call's time)
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
 
 
-class _On:
-    """The device's context for a call (nothing to do where it is current)."""
-
-    def __init__(self, device):
-        self.to = device.index
-        self.back = None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.to:
-            self.back = now
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _run(device, call, *args):
+    """One call with its tensors' device current."""
+    now = torch._C._cuda_getDevice()
+    if now == device.index:
+        return call(*args)
+    torch.cuda.set_device(device)
+    try:
+        return call(*args)
+    finally:
+        torch.cuda.set_device(now)
 
 
 def _device(device):
@@ -143,8 +138,7 @@ class PagedKV:
         self._same_device(batch, ws)
         shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
         ks, vs = _rows(k, shape, "k", self.device), _rows(v, shape, "v", self.device)
-        with _On(self.device):
-            B.lmoe_kv_append(self.cfg, self.c, batch.c, k, v, ks, vs, ws, _stream_of(self.device, stream))
+        _run(self.device, B.lmoe_kv_append, self.cfg, self.c, batch.c, k, v, ks, vs, ws, _stream_of(self.device, stream))
 
     def read(self, batch, ws, out=None, stream=None):
         """(k, v) of the batch's tokens as bf16 values; out: a pair of tensors to write."""
@@ -152,8 +146,7 @@ class PagedKV:
         shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
         k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in "kv")
         ks, vs = _rows(k, shape, "k", self.device), _rows(v, shape, "v", self.device)
-        with _On(self.device):
-            B.lmoe_kv_read(self.cfg, self.c, batch.c, k, v, ks, vs, ws, _stream_of(self.device, stream))
+        _run(self.device, B.lmoe_kv_read, self.cfg, self.c, batch.c, k, v, ks, vs, ws, _stream_of(self.device, stream))
         return k, v
 
     def attend(self, q, batch, ws, scale=None, causal=True, window=0, out=None, lse=None, stream=None):
@@ -165,9 +158,9 @@ class PagedKV:
         out = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if out is None else _whole(out, shape, torch.bfloat16, "out", self.device)
         if lse is not None:
             _whole(lse, shape[:2], torch.float32, "lse", self.device)
-        with _On(self.device):
-            B.lmoe_attend(self.cfg, self.c, batch.c, q, qs, self.head_dim ** -0.5 if scale is None else scale, causal,
-                          window, out, lse, ws, _stream_of(self.device, stream))
+        _run(self.device, B.lmoe_attend, self.cfg, self.c, batch.c, q, qs,
+             self.head_dim ** -0.5 if scale is None else scale, causal, window, out, lse, ws,
+             _stream_of(self.device, stream))
         return out
 
 
@@ -223,8 +216,6 @@ class DeltaStates:
         for t, n in ((log_decay, "log_decay"), (beta, "beta")):
             _whole(t, shape[:2], torch.float32, n, d)
         out = torch.empty(shape, dtype=torch.bfloat16, device=d) if out is None else _whole(out, shape, torch.bfloat16, "out", d)
-        with _On(d):
-            B.lmoe_delta_rule(self.cfg, batch.c, q, k, v, qs, ks, vs, log_decay, beta,
-                              self.head_k ** -0.5 if scale is None else scale, self.state, out, ws,
-                              _stream_of(d, stream))
+        _run(d, B.lmoe_delta_rule, self.cfg, batch.c, q, k, v, qs, ks, vs, log_decay, beta,
+             self.head_k ** -0.5 if scale is None else scale, self.state, out, ws, _stream_of(d, stream))
         return out
