@@ -1,25 +1,27 @@
 // The gated delta rule: S <- a S + b k (v - a k^T S), out = scale S^T q, per
 // head, with the state S [head_k][head_v] in fp32.
 //
-// k_delta_step is the recurrence.  A warp owns 8 columns of a head's state
-// in registers (a lane: 2 columns of DK / 8 rows), so a token is two dot
-// products and one rank-one update in a warp, with shuffles among the lanes
-// that share columns and no exchange between warps.  For a few tokens the
-// state's bytes, read and written once, bound it.
-//
-// The chunked form, for longer sequences: within a chunk of 32 tokens with
-// log decays G_i summed from its start (D_ij = exp(G_i - G_j)), the tokens'
-// updates u solve a unit lower triangular system,
+// All of it in the chunked form: within a chunk of C tokens with log decays
+// G_i summed from its start (D_ij = exp(G_i - G_j)), the tokens' updates u
+// solve a unit lower triangular system,
 //   u_i + sum_{j<i} b_i D_ij (k_i k_j) u_j = b_i (v_i - exp(G_i) k_i S),
 // so with T its inverse and P_ij = scale D_ij (q_i k_j), j <= i,
 //   U = T (b V - b exp(G) K S),  out = scale exp(G) Q S + P U,
 //   S <- exp(G_C) S + (exp(G_C - G) K)^T U.
-// k_delta_chunks makes T, P and the factors of every chunk, k_delta_scan
-// walks a sequence's chunks with S.  Products run on mma.sync m16n8k16 in
-// bf16 (matrices of 32 rows are too small for a tcgen05 tile): q and k are
-// exact operands as they come, what is held in fp32 (S, T, P, U) enters as
-// the sum of two bf16 terms, 2^-17 of its size, with fp32 sums; row norms
-// and decays are applied outside the products.
+// Products run on mma.sync m16n8k16 in bf16 (matrices of 16 and 32 rows are
+// too small for a tcgen05 tile): q and k are exact operands as they come,
+// what is held in fp32 (S, T, P, U) enters as the sum of two bf16 terms,
+// 2^-17 of its size, with fp32 sums; row norms and decays are applied outside
+// the products.  The state is held transposed: with S^T as the first operand
+// a result's registers are the next product's operand as they are.
+//
+// k_delta_short takes a few tokens (one chunk of up to 16) in one launch,
+// bound by the state's bytes, read and written once.  (The plain recurrence,
+// two dot products and a rank-one update a token in fp32, spends 16
+// instructions an element of the state on four tokens where this spends 5,
+// and took 28 us for four tokens of 16 sequences and 32 heads.)
+// For longer sequences k_delta_chunks makes T, P and the factors of every
+// chunk of 32, and k_delta_scan walks a sequence's chunks with S.
 
 #include "lmoe_mixers.cuh"
 #include "lmoe_sm100.cuh"
@@ -28,15 +30,6 @@ namespace lmoe {
 
 namespace {
 
-using sm100::add2;
-using sm100::f2;
-using sm100::fma2;
-using sm100::mul2;
-using sm100::pack2;
-using sm100::unpack2;
-
-constexpr int kStepWarps = 8;
-constexpr int kStepTokens = 8;     // tokens staged at a time
 
 struct DeltaRows {
     int q0, n, src, dst;           // n < 0: the sequence is left out
@@ -56,119 +49,6 @@ __device__ __forceinline__ DeltaRows delta_rows(const DeltaParams& p, int s) {
     }
     return r;
 }
-
-// A CTA: 64 columns of a head's state.
-template <int DK>
-__global__ void __launch_bounds__(kStepWarps * 32, 3) k_delta_step(DeltaParams p) {
-    constexpr int KR = DK / 8;                 // state rows of a lane
-    constexpr int KS = KR + 2;                 // stride of a lane group's rows in shared memory (banks)
-    // (every number twice: a row of the state is a pair of columns, and
-    // arithmetic on pairs halves the instructions, which bound this kernel
-    // before the bytes do: 28 us without it for 16 x 4 tokens of 32 heads)
-    __shared__ __align__(16) float2 s_k[kStepTokens][8 * KS], s_q[kStepTokens][8 * KS];
-    __shared__ float s_a[kStepTokens], s_b[kStepTokens];
-    const int cb = blockIdx.x % (p.DV / 64), sh = blockIdx.x / (p.DV / 64);
-    const int s = sh / p.H, h = sh % p.H, hq = h / p.group;
-    const DeltaRows r = delta_rows(p, s);
-    if (r.n < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kg = lane >> 2, c0 = cb * 64 + warp * 8 + (lane & 3) * 2;   // rows kg * KR .., columns c0, c0 + 1
-    f2 S[KR];
-    if (r.src >= 0) {
-        const float* src = p.states + (((size_t)r.src * p.H + h) * DK + kg * KR) * p.DV + c0;
-#pragma unroll
-        for (int i = 0; i < KR; ++i) {
-            const float2 v = *reinterpret_cast<const float2*>(src + (size_t)i * p.DV);
-            S[i] = pack2(v.x, v.y);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < KR; ++i) S[i] = 0ull;
-    }
-    for (int t0 = 0; t0 < r.n; t0 += kStepTokens) {
-        const int nt = min(kStepTokens, r.n - t0);
-        __syncthreads();
-        for (int j = warp; j < 2 * nt; j += kStepWarps) {
-            const int tok = j >> 1;
-            const bool isq = j & 1;
-            const uint16_t* x = isq ? p.q + (size_t)(r.q0 + t0 + tok) * p.qs : p.k + (size_t)(r.q0 + t0 + tok) * p.ks;
-            x += (size_t)hq * DK;
-            float v[DK / 32], sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < DK / 64; ++i) {
-                const float2 f = bf16x2_to_f32x2(__ldg(reinterpret_cast<const uint32_t*>(x) + lane * (DK / 64) + i));
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-                sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
-            }
-            float f = isq ? p.scale : 1.f;
-            if (p.l2norm) f *= 1.f / sqrtf(warp_sum(sum) + 1e-6f);
-            float2* dst = isq ? s_q[tok] : s_k[tok];
-#pragma unroll
-            for (int i = 0; i < DK / 32; ++i) {
-                const int d = lane * (DK / 32) + i;
-                dst[(d / KR) * KS + d % KR] = make_float2(v[i] * f, v[i] * f);
-            }
-        }
-        if (threadIdx.x < nt) {
-            const size_t at = (size_t)(r.q0 + t0 + threadIdx.x) * p.H + h;
-            s_a[threadIdx.x] = expf(p.log_decay[at]);
-            s_b[threadIdx.x] = p.beta[at];
-        }
-        __syncthreads();
-        for (int j = 0; j < nt; ++j) {
-            const size_t row = (size_t)(r.q0 + t0 + j);
-            const float2 v = bf16x2_to_f32x2(
-                __ldg(reinterpret_cast<const uint32_t*>(p.v + row * p.vs + (size_t)h * p.DV + c0)));
-            const float a = s_a[j], b = s_b[j];
-            const ulonglong2* kp = reinterpret_cast<const ulonglong2*>(&s_k[j][kg * KS]);
-            const ulonglong2* qp = reinterpret_cast<const ulonglong2*>(&s_q[j][kg * KS]);
-            f2 xa = 0ull, xb = 0ull;
-#pragma unroll
-            for (int i = 0; i < KR; i += 2) {
-                const ulonglong2 k = kp[i / 2];
-                xa = fma2(k.x, S[i], xa);
-                xb = fma2(k.y, S[i + 1], xb);
-            }
-            float2 x = unpack2(add2(xa, xb));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-                x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-            }
-            // (the state's own product with the decay comes with the update)
-            const f2 u = pack2((v.x - a * x.x) * b, (v.y - a * x.y) * b), a2 = pack2(a, a);
-            xa = xb = 0ull;
-#pragma unroll
-            for (int i = 0; i < KR; i += 2) {
-                const ulonglong2 k = kp[i / 2], q = qp[i / 2];
-                S[i] = fma2(k.x, u, mul2(S[i], a2));
-                S[i + 1] = fma2(k.y, u, mul2(S[i + 1], a2));
-                xa = fma2(q.x, S[i], xa);
-                xb = fma2(q.y, S[i + 1], xb);
-            }
-            x = unpack2(add2(xa, xb));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-                x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-            }
-            if (kg == 0)
-                *reinterpret_cast<uint32_t*>(p.out + (row * p.H + h) * p.DV + c0) =
-                    (uint32_t)f32_to_bf16_bits(x.x) | (uint32_t)f32_to_bf16_bits(x.y) << 16;
-        }
-    }
-    if (r.dst >= 0 && (r.n > 0 || r.dst != r.src)) {
-        float* dst = p.states + (((size_t)r.dst * p.H + h) * DK + kg * KR) * p.DV + c0;
-#pragma unroll
-        for (int i = 0; i < KR; ++i) *reinterpret_cast<float2*>(dst + (size_t)i * p.DV) = unpack2(S[i]);
-    }
-}
-
-
-// ---------------------------------------------------------------------------
-// chunked form
-// ---------------------------------------------------------------------------
 
 constexpr int kC = 32;                       // tokens of a chunk
 
@@ -234,18 +114,33 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& high, uint32_
     const float2 h = bf16x2_to_f32x2(high);
     low = pack_bf16(x - h.x, y - h.y);
 }
+// The two terms of 16 rows x 16 columns of results as a first operand.
+__device__ __forceinline__ void split_a(const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split2(x[0], x[1], hi[0], lo[0]);
+    split2(x[2], x[3], hi[1], lo[1]);
+    split2(y[0], y[1], hi[2], lo[2]);
+    split2(y[2], y[3], hi[3], lo[3]);
+}
+// An 8 x 8 matrix of 16-bit numbers, two a lane, transposed: pairs of tokens
+// of a column become pairs of columns of a token.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// W elements of each row of a chunk (n_here rows, zeros behind) to shared memory.
-template <int W, int STRIDE>
+// W elements of each of ROWS rows (n_here there, zeros behind) to shared memory.
+template <int W, int STRIDE, int ROWS = kC>
 __device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, size_t stride, int n_here, int nt) {
 #pragma unroll
-    for (int i0 = 0; i0 < kC * W / 8; i0 += nt) {
+    for (int i0 = 0; i0 < ROWS * W / 8; i0 += nt) {
         const int i = i0 + threadIdx.x;
+        if (ROWS * W / 8 % nt && i >= ROWS * W / 8) break;
         const int r = i / (W / 8), c = i % (W / 8) * 8;
         if (r < n_here) cp_async16(dst + r * STRIDE + c, src + (size_t)r * stride + c);
         else *reinterpret_cast<uint4*>(dst + r * STRIDE + c) = make_uint4(0, 0, 0, 0);
@@ -474,6 +369,290 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
     }
 }
 
+// ---------------------------------------------------------------------------
+// a few tokens
+// ---------------------------------------------------------------------------
+
+constexpr int kFew = 16;                     // tokens, at most
+constexpr int kShortThreads = 128;
+constexpr int kShortN = 64;                  // state columns of a block, 16 a warp
+
+// Block: 64 columns of a head's state.  Its loads are issued first and arrive
+// while the chunk's matrices are made.
+template <int DK>
+__global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p) {
+    constexpr int NT = DK / 8;
+    __shared__ __align__(16) uint16_t sk[kFew][DK + 8], sq[kFew][DK + 8], sv[kFew][kShortN + 8];
+    __shared__ __align__(16) float kk[kFew][kFew + 4], qk[kFew][kFew + 4], sa[kFew][kFew + 4];
+    __shared__ __align__(16) uint4 s_t[2][32], s_p[2][32];
+    __shared__ __align__(16) float s_b[kFew], s_kf[kFew], s_qf[kFew], s_wf[kFew];
+    __shared__ float s_rk[kFew], s_rq[kFew], s_gh[2][kFew], s_gl[2][kFew], s_last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nb = p.DV / kShortN, cb = blockIdx.x % nb, sh = blockIdx.x / nb;
+    const int s = sh / p.H, h = sh % p.H, hq = h / p.group;
+    const DeltaRows r = delta_rows(p, s);
+    if (r.n < 0) return;
+    // element (column g + 8 i, row 8 j + 2 t + e) of this warp's 16 columns
+    const size_t state_at = ((size_t)h * DK + 2 * t) * p.DV + cb * kShortN + warp * 16 + g;
+    float S[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[j][i] = 0.f;
+    if (r.src >= 0) {
+        const float* src = p.states + (size_t)r.src * p.H * DK * p.DV + state_at;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[j][i] = src[(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)];
+    }
+    if (r.n > 0) {
+        load_rows<DK, DK + 8, kFew>(&sk[0][0], p.k + (size_t)r.q0 * p.ks + (size_t)hq * DK, p.ks, r.n, kShortThreads);
+        load_rows<DK, DK + 8, kFew>(&sq[0][0], p.q + (size_t)r.q0 * p.qs + (size_t)hq * DK, p.qs, r.n, kShortThreads);
+        load_rows<kShortN, kShortN + 8, kFew>(&sv[0][0], p.v + (size_t)r.q0 * p.vs + (size_t)h * p.DV + cb * kShortN, p.vs, r.n,
+                                              kShortThreads);
+        cp_async_commit();
+        // ---- decays (warps 0 and 1; a lane a token), as in k_delta_chunks
+        float gh = 0.f, gl = 0.f, b = 0.f;
+        if (warp < 2) {
+            const size_t at = (size_t)(r.q0 + min(lane, r.n - 1)) * p.H + h;
+            float gt = lane < r.n ? p.log_decay[at] : 0.f;
+            b = lane < r.n ? p.beta[at] : 0.f;
+            if (gt < -128.f) gt = -128.f;
+            gh = rintf(gt * 8.f) * 0.125f;
+            gl = gt - gh;
+#pragma unroll
+            for (int o = 1; o < kFew; o <<= 1) {
+                const float yh = __shfl_up_sync(0xffffffffu, gh, o), yl = __shfl_up_sync(0xffffffffu, gl, o);
+                if (lane >= o) { gh += yh; gl += yl; }
+            }
+            if (lane < kFew) {
+                s_gh[warp][lane] = gh;
+                s_gl[warp][lane] = gl;
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();
+        // ---- K K^T (warp 0), Q K^T (1), norms of q (2)
+        if (warp < 2) {
+            const uint16_t(*a_rows)[DK + 8] = warp ? sq : sk;
+            float acc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
+                uint32_t a[4], y[4];
+                ldm4(a, &a_rows[lane & 15][16 * k + (lane >> 4) * 8]);
+                ldm4(y, &sk[(lane & 7) + (lane >> 4) * 8][16 * k + ((lane >> 3) & 1) * 8]);
+                mma_bf16(acc[0], a, y[0], y[1]);
+                mma_bf16(acc[1], a, y[2], y[3]);
+            }
+            float(*dst)[kFew + 4] = warp ? qk : kk;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<float2*>(&dst[g + 8 * i][8 * j + 2 * t]) = make_float2(acc[j][2 * i], acc[j][2 * i + 1]);
+        } else if (warp == 2) {
+            const int row = lane >> 1;
+            float nq = 0.f;
+#pragma unroll 8
+            for (int i = 0; i < DK / 4; ++i) {
+                const float2 x = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sq[row][2 * ((lane & 1) + 2 * i)]));
+                nq = fmaf(x.x, x.x, fmaf(x.y, x.y, nq));
+            }
+            nq += __shfl_xor_sync(0xffffffffu, nq, 1);
+            if (!(lane & 1)) s_rq[row] = p.scale * (p.l2norm ? 1.f / sqrtf(nq + 1e-6f) : 1.f);
+        }
+        __syncthreads();
+        // ---- T (warp 0), P and factors (warp 1)
+        if (warp < 2) {
+            const float* xh = s_gh[warp];
+            const float* xl = s_gl[warp];
+            const int tok = lane & 15;
+            gh = xh[tok];
+            gl = xl[tok];
+            b = __shfl_sync(0xffffffffu, b, tok);
+            const float rk = p.l2norm ? 1.f / sqrtf(kk[tok][tok] + 1e-6f) : 1.f;
+            if (warp == 0) {
+                const float br = b * rk;
+                float x[kFew];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kFew; ++i) {             // column `tok` of b_i D_ij (k_i k_j)
+                    const float bi = __shfl_sync(0xffffffffu, br, i);
+                    x[i] = tok < i ? kk[i][tok] * (bi * rk) * exp_of((xh[i] - gh) + (xl[i] - gl)) : 0.f;
+                }
+                __syncwarp();
+                if (lane < kFew)
+#pragma unroll
+                    for (int i = 0; i < kFew; ++i) sa[i][lane] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kFew; ++i) {             // and of the inverse, from the top
+                    float y[4] = {i == tok ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < i; j += 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(&sa[i][j]);          // (zeros from column i on)
+                        y[0] = fmaf(-a.x, x[j], y[0]);
+                        if (j + 1 < i) y[1] = fmaf(-a.y, x[j + 1], y[1]);
+                        if (j + 2 < i) y[2] = fmaf(-a.z, x[j + 2], y[2]);
+                        if (j + 3 < i) y[3] = fmaf(-a.w, x[j + 3], y[3]);
+                    }
+                    x[i] = (y[0] + y[1]) + (y[2] + y[3]);
+                }
+                __syncwarp();
+                if (lane < kFew)
+#pragma unroll
+                    for (int i = 0; i < kFew; ++i) sa[i][lane] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 u0 = *reinterpret_cast<const float2*>(&sa[8 * j + g][2 * t]);
+                    const float2 u1 = *reinterpret_cast<const float2*>(&sa[8 * j + g][2 * t + 8]);
+                    uint4 w;
+                    split2(u0.x, u0.y, w.x, w.z);
+                    split2(u1.x, u1.y, w.y, w.w);
+                    s_t[j][lane] = w;
+                }
+            } else {
+                const float e = exp_of(gh + gl), w = exp_of((xh[kFew - 1] - gh) + (xl[kFew - 1] - gl));
+                if (lane < kFew) {
+                    s_b[lane] = b;
+                    s_kf[lane] = b * e * rk;
+                    s_qf[lane] = e * s_rq[lane];
+                    s_wf[lane] = w * rk;
+                    s_rk[lane] = rk;
+                    if (lane == kFew - 1) s_last = e;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int i = 8 * j + g;
+                    float u[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = 2 * t + (c & 1) + 8 * (c >> 1);
+                        const float d = exp_of((xh[i] - xh[col]) + (xl[i] - xl[col]));
+                        u[c] = col <= i ? qk[i][col] * (s_rq[i] * s_rk[col]) * d : 0.f;
+                    }
+                    uint4 x;
+                    split2(u[0], u[1], x.x, x.z);
+                    split2(u[2], u[3], x.y, x.w);
+                    s_p[j][lane] = x;
+                }
+            }
+        }
+        __syncthreads();
+        // ---- (K S)^T, (Q S)^T: 16 columns x 16 tokens
+        float ks[2][4], qs[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ks[j][i] = qs[j][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
+            uint32_t hi[4], lo[4], bk[4], bq[4];
+            split_a(S[2 * k], S[2 * k + 1], hi, lo);
+            const int col = 16 * k + ((lane >> 3) & 1) * 8;
+            ldm4(bk, &sk[(lane & 7) + (lane >> 4) * 8][col]);
+            ldm4(bq, &sq[(lane & 7) + (lane >> 4) * 8][col]);
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    mma_bf16(ks[j], o ? lo : hi, bk[2 * j], bk[2 * j + 1]);
+                    mma_bf16(qs[j], o ? lo : hi, bq[2 * j], bq[2 * j + 1]);
+                }
+        }
+        // ---- right-hand sides over K S, U^T
+        float u[2][4], o[2][4];
+        uint32_t v[4], hi[4], lo[4];
+        ldm4t(v, &sv[lane & 15][warp * 16 + (lane >> 4) * 8]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 bb = *reinterpret_cast<const float2*>(&s_b[8 * j + 2 * t]);
+            const float2 f = *reinterpret_cast<const float2*>(&s_kf[8 * j + 2 * t]);
+            const float2 q = *reinterpret_cast<const float2*>(&s_qf[8 * j + 2 * t]);
+            const float2 v0 = bf16x2_to_f32x2(v[j]), v1 = bf16x2_to_f32x2(v[2 + j]);
+            ks[j][0] = fmaf(-f.x, ks[j][0], bb.x * v0.x);
+            ks[j][1] = fmaf(-f.y, ks[j][1], bb.y * v0.y);
+            ks[j][2] = fmaf(-f.x, ks[j][2], bb.x * v1.x);
+            ks[j][3] = fmaf(-f.y, ks[j][3], bb.y * v1.y);
+            o[j][0] = q.x * qs[j][0];
+            o[j][1] = q.y * qs[j][1];
+            o[j][2] = q.x * qs[j][2];
+            o[j][3] = q.y * qs[j][3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
+        }
+        split_a(ks[0], ks[1], hi, lo);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 f = s_t[j][lane];
+            mma_bf16(u[j], hi, f.x, f.y);
+            mma_bf16(u[j], hi, f.z, f.w);
+            mma_bf16(u[j], lo, f.x, f.y);
+        }
+        // ---- out^T
+        split_a(u[0], u[1], hi, lo);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 f = s_p[j][lane];
+            mma_bf16(o[j], hi, f.x, f.y);
+            mma_bf16(o[j], hi, f.z, f.w);
+            mma_bf16(o[j], lo, f.x, f.y);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t y = transposed(pack_bf16(o[j][2 * i], o[j][2 * i + 1]));
+                const int row = 8 * j + g;
+                if (row < r.n)
+                    *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kShortN + warp * 16 + 8 * i +
+                                                 2 * t) = y;
+            }
+        // ---- the state
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 f = *reinterpret_cast<const float2*>(&s_wf[8 * j + 2 * t]);
+            u[j][0] *= f.x;
+            u[j][1] *= f.y;
+            u[j][2] *= f.x;
+            u[j][3] *= f.y;
+        }
+        split_a(u[0], u[1], hi, lo);
+        const float last = s_last;
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+            uint32_t bk[4];
+            ldm4t(bk, &sk[lane & 15][16 * j + (lane >> 4) * 8]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float(&x)[4] = S[2 * j + i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] *= last;
+                mma_bf16(x, hi, bk[2 * i], bk[2 * i + 1]);
+                mma_bf16(x, lo, bk[2 * i], bk[2 * i + 1]);
+            }
+        }
+    }
+    if (r.dst >= 0 && (r.n > 0 || r.dst != r.src)) {
+        float* dst = p.states + (size_t)r.dst * p.H * DK * p.DV + state_at;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)] = S[j][i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// a sequence's chunks
+// ---------------------------------------------------------------------------
+
 constexpr int kScanThreads = 160;           // four warps compute, the fifth loads
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 constexpr int kN = 32;                       // state columns of a block
@@ -490,9 +669,7 @@ struct Scan {
     int abort;
 };
 
-// Block: kN columns of a head's state, transposed: with S^T as the first
-// operand a result's registers are the next product's operand as they are.
-// Two warps hold 16 columns, half of the state's rows each, in fp32 registers
+// Block: kN columns of a head's state.  Two warps hold 16 columns, half of the state's rows each, in fp32 registers
 // from the first chunk to the last; they add up their shares of K S and Q S
 // through shared memory, both compute U, and each updates its rows of S and
 // writes half of the tokens.  The chain of a chunk's steps bounds it (about
@@ -561,12 +738,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int i = 0; i < 4; ++i) S[j][i] = src[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)];
     }
-    auto split_a = [&](const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-        split2(x[0], x[1], hi[0], lo[0]);
-        split2(x[2], x[3], hi[1], lo[1]);
-        split2(y[0], y[1], hi[2], lo[2]);
-        split2(y[2], y[3], hi[3], lo[3]);
-    };
     bool dead = false;
     for (int c = 0; c < n_chunks; ++c) {
         dead = !sm100::mbar_wait(&sm.full[c & 1], (c >> 1) & 1, abort, kWaitLimit);
@@ -726,10 +897,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                // (token 2 t, 2 t + 1 of column g) -> (columns 2 t, 2 t + 1 of token g)
-                uint32_t y;
-                const uint32_t z = pack_bf16(o[j][2 * i], o[j][2 * i + 1]);
-                asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(z));
+                const uint32_t y = transposed(pack_bf16(o[j][2 * i], o[j][2 * i + 1]));
                 const int row = c * kC + 16 * hf + 8 * j + g;
                 if (row < r.n)
                     *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kN + gp * 16 + 8 * i + 2 * t) = y;
@@ -747,9 +915,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             for (int i = 0; i < 4; ++i) dst[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)] = S[j][i];
     }
 }
-
-// More new tokens than this per sequence run the chunked form.
-constexpr int kStepTokensMax = 16;
 
 int chunk_slots(int n_tokens, int n_seqs) {
     const long long n = (long long)n_tokens / kC + n_seqs;
@@ -781,14 +946,14 @@ cudaError_t run_chunks(const DeltaParams& p, cudaStream_t st) {
 }  // namespace
 
 size_t delta_chunk_ws_bytes(int H, int n_tokens, int n_seqs, int max_new) {
-    return max_new <= kStepTokensMax ? 0 : sizeof(ChunkData) * (size_t)chunk_slots(n_tokens, n_seqs) * H;
+    return max_new <= kFew ? 0 : sizeof(ChunkData) * (size_t)chunk_slots(n_tokens, n_seqs) * H;
 }
 
 cudaError_t run_delta(const DeltaParams& p, cudaStream_t st) {
-    if (p.max_new > kStepTokensMax) return p.DK == 64 ? run_chunks<64>(p, st) : run_chunks<128>(p, st);
-    const unsigned g = (unsigned)((size_t)p.n_seqs * p.H * (p.DV / 64));
-    if (p.DK == 64) k_delta_step<64><<<g, kStepWarps * 32, 0, st>>>(p);
-    else k_delta_step<128><<<g, kStepWarps * 32, 0, st>>>(p);
+    if (p.max_new > kFew) return p.DK == 64 ? run_chunks<64>(p, st) : run_chunks<128>(p, st);
+    const unsigned g = (unsigned)((size_t)p.n_seqs * p.H * (p.DV / kShortN));
+    if (p.DK == 64) k_delta_short<64><<<g, kShortThreads, 0, st>>>(p);
+    else k_delta_short<128><<<g, kShortThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
