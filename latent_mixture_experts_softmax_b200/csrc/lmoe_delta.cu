@@ -9,10 +9,13 @@
 //   U = T (b V - b exp(G) K S),  out = scale exp(G) Q S + P U,
 //   S <- exp(G_C) S + (exp(G_C - G) K)^T U.
 // Products run on mma.sync m16n8k16 in bf16 (matrices of 16 and 32 rows are
-// too small for a tcgen05 tile): q and k are exact operands as they come,
-// what is held in fp32 (S, T, P, U) enters as the sum of two bf16 terms,
-// 2^-17 of its size, with fp32 sums; row norms and decays are applied outside
-// the products.  The state is held transposed: with S^T as the first operand
+// too small for a tcgen05 tile): q and k are exact operands as they come.
+// What is held in fp32 and goes into the state (S in K S, T, the right-hand
+// sides, U) enters as the sum of three bf16 terms, all 24 bits; what only
+// goes into the outputs, which are bf16, as two (2^-17 of its size).  Sums
+// are fp32, and the tensor cores, which truncate where they add, never add to
+// the state itself: S exp(G_C) + delta is one rounded fma an element.  Row
+// norms and decays are applied outside the products.  The state is held transposed: with S^T as the first operand
 // a result's registers are the next product's operand as they are.
 //
 // k_delta_short takes a few tokens (one chunk of up to 16) in one launch,
@@ -55,9 +58,11 @@ constexpr int kC = 32;                       // tokens of a chunk
 // What k_delta_chunks leaves of a chunk and head.  T and P as the second
 // operand of a product: tile (k, j), 16 x 8, holds rows 8 j .. of the matrix at
 // columns 16 k .. (tiles that are not zero: 0..3 = (0, j), 4, 5 = (1, 2), (1, 3)),
-// 16 bytes a lane: the two registers of the high terms, then of the low.
+// 16 bytes a lane: the two registers of the high terms, then of the next; of T
+// the lowest terms too.
 struct ChunkData {
     uint4 t[6][32], p[6][32];
+    uint2 tl[6][32];
     float b[kC], kf[kC], qf[kC], wf[kC];     // b, b exp(G) |k|^-1, scale exp(G) |q|^-1, exp(G_C - G) |k|^-1
     float last[4];                           // exp(G_C)
 };
@@ -114,12 +119,33 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& high, uint32_
     const float2 h = bf16x2_to_f32x2(high);
     low = pack_bf16(x - h.x, y - h.y);
 }
+// As the sum of three: every bit.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& high, uint32_t& mid, uint32_t& low) {
+    high = pack_bf16(x, y);
+    const float2 h = bf16x2_to_f32x2(high);
+    split2(x - h.x, y - h.y, mid, low);
+}
+__device__ __forceinline__ void split_a(const float (&x)[4], const float (&y)[4], uint32_t (&a)[3][4]) {
+    split3(x[0], x[1], a[0][0], a[1][0], a[2][0]);
+    split3(x[2], x[3], a[0][1], a[1][1], a[2][1]);
+    split3(y[0], y[1], a[0][2], a[1][2], a[2][2]);
+    split3(y[2], y[3], a[0][3], a[1][3], a[2][3]);
+}
 // The two terms of 16 rows x 16 columns of results as a first operand.
 __device__ __forceinline__ void split_a(const float (&x)[4], const float (&y)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     split2(x[0], x[1], hi[0], lo[0]);
     split2(x[2], x[3], hi[1], lo[1]);
     split2(y[0], y[1], hi[2], lo[2]);
     split2(y[2], y[3], hi[3], lo[3]);
+}
+// acc += A B from three terms each: the six products that count, small first.
+__device__ __forceinline__ void mul3(float (&acc)[4], const uint32_t (&a)[3][4], const uint4& b, const uint2& bl) {
+    mma_bf16(acc, a[2], b.x, b.y);
+    mma_bf16(acc, a[1], b.z, b.w);
+    mma_bf16(acc, a[0], bl.x, bl.y);
+    mma_bf16(acc, a[1], b.x, b.y);
+    mma_bf16(acc, a[0], b.z, b.w);
+    mma_bf16(acc, a[0], b.x, b.y);
 }
 // An 8 x 8 matrix of 16-bit numbers, two a lane, transposed: pairs of tokens
 // of a column become pairs of columns of a token.
@@ -337,9 +363,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                     const float2 u0 = *reinterpret_cast<const float2*>(&m[8 * j + g][16 * k + 2 * t]);
                     const float2 u1 = *reinterpret_cast<const float2*>(&m[8 * j + g][16 * k + 2 * t + 8]);
                     uint4 w;
-                    split2(u0.x, u0.y, w.x, w.z);
-                    split2(u1.x, u1.y, w.y, w.w);
+                    uint2 l;
+                    split3(u0.x, u0.y, w.x, w.z, l.x);
+                    split3(u1.x, u1.y, w.y, w.w, l.y);
                     out->t[tile][lane] = w;
+                    out->tl[tile][lane] = l;
                 }
             } else {
                 const float e = exp_of(gh + gl);
@@ -385,6 +413,7 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
     __shared__ __align__(16) uint16_t sk[kFew][DK + 8], sq[kFew][DK + 8], sv[kFew][kShortN + 8];
     __shared__ __align__(16) float kk[kFew][kFew + 4], qk[kFew][kFew + 4], sa[kFew][kFew + 4];
     __shared__ __align__(16) uint4 s_t[2][32], s_p[2][32];
+    __shared__ uint2 s_tl[2][32];
     __shared__ __align__(16) float s_b[kFew], s_kf[kFew], s_qf[kFew], s_wf[kFew];
     __shared__ float s_rk[kFew], s_rq[kFew], s_gh[2][kFew], s_gl[2][kFew], s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -513,9 +542,11 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
                     const float2 u0 = *reinterpret_cast<const float2*>(&sa[8 * j + g][2 * t]);
                     const float2 u1 = *reinterpret_cast<const float2*>(&sa[8 * j + g][2 * t + 8]);
                     uint4 w;
-                    split2(u0.x, u0.y, w.x, w.z);
-                    split2(u1.x, u1.y, w.y, w.w);
+                    uint2 l;
+                    split3(u0.x, u0.y, w.x, w.z, l.x);
+                    split3(u1.x, u1.y, w.y, w.w, l.y);
                     s_t[j][lane] = w;
+                    s_tl[j][lane] = l;
                 }
             } else {
                 const float e = exp_of(gh + gl), w = exp_of((xh[kFew - 1] - gh) + (xl[kFew - 1] - gl));
@@ -554,17 +585,17 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
             for (int i = 0; i < 4; ++i) ks[j][i] = qs[j][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < DK / 16; ++k) {
-            uint32_t hi[4], lo[4], bk[4], bq[4];
-            split_a(S[2 * k], S[2 * k + 1], hi, lo);
+            uint32_t a[3][4], bk[4], bq[4];
+            split_a(S[2 * k], S[2 * k + 1], a);
             const int col = 16 * k + ((lane >> 3) & 1) * 8;
             ldm4(bk, &sk[(lane & 7) + (lane >> 4) * 8][col]);
             ldm4(bq, &sq[(lane & 7) + (lane >> 4) * 8][col]);
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
+            for (int o = 0; o < 3; ++o)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    mma_bf16(ks[j], o ? lo : hi, bk[2 * j], bk[2 * j + 1]);
-                    mma_bf16(qs[j], o ? lo : hi, bq[2 * j], bq[2 * j + 1]);
+                    mma_bf16(ks[j], a[o], bk[2 * j], bk[2 * j + 1]);
+                    if (o < 2) mma_bf16(qs[j], a[o], bq[2 * j], bq[2 * j + 1]);
                 }
         }
         // ---- right-hand sides over K S, U^T
@@ -588,13 +619,13 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
         }
-        split_a(ks[0], ks[1], hi, lo);
+        uint32_t a[3][4];
+        split_a(ks[0], ks[1], a);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint4 f = s_t[j][lane];
-            mma_bf16(u[j], hi, f.x, f.y);
-            mma_bf16(u[j], hi, f.z, f.w);
-            mma_bf16(u[j], lo, f.x, f.y);
+            const uint2 l = s_tl[j][lane];
+            mul3(u[j], a, f, l);
         }
         // ---- out^T
         split_a(u[0], u[1], hi, lo);
@@ -624,7 +655,7 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
             u[j][2] *= f.x;
             u[j][3] *= f.y;
         }
-        split_a(u[0], u[1], hi, lo);
+        split_a(u[0], u[1], a);
         const float last = s_last;
 #pragma unroll
         for (int j = 0; j < NT / 2; ++j) {
@@ -632,11 +663,11 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
             ldm4t(bk, &sk[lane & 15][16 * j + (lane >> 4) * 8]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float(&x)[4] = S[2 * j + i];
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] *= last;
-                mma_bf16(x, hi, bk[2 * i], bk[2 * i + 1]);
-                mma_bf16(x, lo, bk[2 * i], bk[2 * i + 1]);
+                for (int o = 2; o >= 0; --o) mma_bf16(d, a[o], bk[2 * i], bk[2 * i + 1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[2 * j + i][e] = fmaf(S[2 * j + i][e], last, d[e]);
             }
         }
     }
@@ -752,8 +783,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             for (int i = 0; i < 4; ++i) ks[j][i] = qs[j][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < KH / 16; ++k) {
-            uint32_t hi[4], lo[4];
-            split_a(S[2 * k], S[2 * k + 1], hi, lo);
+            uint32_t a[3][4];
+            split_a(S[2 * k], S[2 * k + 1], a);
             const int col = hf * KH + 16 * k + ((lane >> 3) & 1) * 8;
             uint32_t bk[2][4], bq[2][4];
 #pragma unroll
@@ -763,11 +794,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             }
             // (products that add to the same sums stand far apart here and below)
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
+            for (int o = 0; o < 3; ++o)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    mma_bf16(ks[j], o ? lo : hi, bk[j >> 1][2 * (j & 1)], bk[j >> 1][2 * (j & 1) + 1]);
-                    mma_bf16(qs[j], o ? lo : hi, bq[j >> 1][2 * (j & 1)], bq[j >> 1][2 * (j & 1) + 1]);
+                    mma_bf16(ks[j], a[o], bk[j >> 1][2 * (j & 1)], bk[j >> 1][2 * (j & 1) + 1]);
+                    if (o < 2) mma_bf16(qs[j], a[o], bq[j >> 1][2 * (j & 1)], bq[j >> 1][2 * (j & 1) + 1]);
                 }
         }
         // ---- the partner's share: all of K S, and Q S of the tokens this warp writes
@@ -838,42 +869,65 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            uint32_t hi[4], lo[4];
-            split_a(ks[2 * k], ks[2 * k + 1], hi, lo);
+            uint32_t a[3][4];
+            split_a(ks[2 * k], ks[2 * k + 1], a);
             const uint4* f = ft + 2 * k;
+            uint2 l[4];
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], hi, f[j].x, f[j].y);
+            for (int j = 2 * k; j < 4; ++j) l[j] = x.d.tl[k ? j + 2 : j][lane];
+            // (mul3, of up to four tiles side by side)
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], hi, f[j].z, f[j].w);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[2], f[j].x, f[j].y);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], lo, f[j].x, f[j].y);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].z, f[j].w);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], l[j].x, l[j].y);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].x, f[j].y);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].z, f[j].w);
+#pragma unroll
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].x, f[j].y);
         }
         // ---- the state
         const float last = x.d.last[0];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[j][i] *= last;
+        uint32_t w[2][3][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float w[2][4];
+            float y[2][4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float2 f = *reinterpret_cast<const float2*>(&x.d.wf[16 * k + 8 * j + 2 * t]);
-                w[j][0] = f.x * u[2 * k + j][0];
-                w[j][1] = f.y * u[2 * k + j][1];
-                w[j][2] = f.x * u[2 * k + j][2];
-                w[j][3] = f.y * u[2 * k + j][3];
+                y[j][0] = f.x * u[2 * k + j][0];
+                y[j][1] = f.y * u[2 * k + j][1];
+                y[j][2] = f.x * u[2 * k + j][2];
+                y[j][3] = f.y * u[2 * k + j][3];
             }
-            uint32_t hi[4], lo[4];
-            split_a(w[0], w[1], hi, lo);
-            uint32_t bk[NT / 2][4];
+            split_a(y[0], y[1], w[k]);
+        }
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) ldm4t(bk[j], &x.k[16 * k + (lane & 15)][hf * KH + 16 * j + (lane >> 4) * 8]);
+        for (int j0 = 0; j0 < NT; j0 += 4) {             // 32 rows of the state at a time
+            uint32_t bk[2][2][4];
 #pragma unroll
-            for (int o = 0; o < 2; ++o)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma_bf16(S[j], o ? lo : hi, bk[j >> 1][2 * (j & 1)], bk[j >> 1][2 * (j & 1) + 1]);
+                for (int j = 0; j < 2; ++j)
+                    ldm4t(bk[k][j], &x.k[16 * k + (lane & 15)][hf * KH + 8 * j0 + 16 * j + (lane >> 4) * 8]);
+            float d[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_bf16(d[j], w[k][o], bk[k][j >> 1][2 * (j & 1)], bk[k][j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[j0 + j][i] = fmaf(S[j0 + j][i], last, d[j][i]);
         }
         // ---- out^T of 16 tokens
 #pragma unroll
