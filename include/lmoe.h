@@ -413,8 +413,10 @@ LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, c
 /* The gated delta rule over the new tokens of n_seqs sequences, each with a
  * state S [head_k][head_v] per head:
  *   S <- exp(log_decay) S;  S <- S + beta k (v - k^T S);  out = scale S^T q
- * A token step of a few tokens runs the recurrence, longer sequences its
- * chunked form; both hold the state and every sum that enters it in fp32. */
+ * Batches with max_new up to 16 run in one launch, longer sequences in chunks
+ * of 32 tokens.  The state and every sum are fp32; fp32 operands that go into
+ * the state enter the products with all their bits, those that only go into
+ * out with 16.  Results do not depend on timing. */
 typedef struct {
     int n_heads;       /* heads of v, the gates and the state: a multiple of n_qk_heads */
     int n_qk_heads;    /* heads of q and k; head j uses q, k head j / (n_heads / n_qk_heads) */

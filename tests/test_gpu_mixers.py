@@ -459,3 +459,154 @@ def test_another_stream_and_a_replayed_graph_with_other_lengths():
         for s in range(2):
             want, _, tol, _ = R.attend(q[s:s + 1], cache.rows("k", s, pair[s]), cache.rows("v", s, pair[s]), pair[s] - 1, 128 ** -0.5, True, 0)
             R.assert_within(out[s:s + 1], want, tol, f"lengths {pair}")
+
+
+def graphed(step):
+    """step() captured on a side stream, after one eager run."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    return graph
+
+
+@pytest.mark.parametrize("n", [70, 150])
+def test_a_replayed_graph_of_prompt_chunks(n):
+    """Attention of many rows (one row tile, and more than four) and the chunked delta rule, replayed with other lengths."""
+    cache = R.Cache("e4m3", 1, 64, 16, [400, 300])
+    pk = paged(cache, 8, 1, 64)
+    ws = pk.workspace()
+    q = torch.randn(2 * n, 8, 64, generator=torch.Generator().manual_seed(n)).bfloat16()
+    dq, table = q.to(DEV), cache.table.to(DEV)
+    starts, lens = R.starts([n, n]).to(DEV), torch.tensor([400, 300], dtype=torch.int32, device=DEV)
+    b = pk.batch(starts, lens, table, 2 * n, n)
+    out = torch.empty(2 * n, 8, 64, dtype=torch.bfloat16, device=DEV)
+    H, DK = 2, 64
+    x = delta_inputs(2 * n, H, 1, DK, DK, 5, l2norm=True)
+    S = torch.randn(2, H, DK, DK, generator=torch.Generator().manual_seed(6))
+    st = mixers.DeltaStates(H, 1, DK, DK, l2norm=True, state=torch.cat([S, S]).to(DEV))
+    dws = st.workspace(2 * n, 2, n)
+    dx = [t.to(DEV) for t in x]
+    src, dst = (torch.tensor(i, dtype=torch.int32, device=DEV) for i in ([0, 1], [2, 3]))
+    db = st.batch(starts, src, dst, 2 * n, n)
+    dout = torch.empty(2 * n, H, DK, dtype=torch.bfloat16, device=DEV)
+
+    def step():
+        pk.attend(dq, b, ws, out=out)
+        st.forward(*dx, db, dws, out=dout)
+
+    graph = graphed(step)
+    for ns, kv in (([n, n], [400, 300]), ([n, 1], [n, 17]), ([3, n - 5], [400, 299])):
+        starts.copy_(R.starts(ns))
+        lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        out.fill_(5.0)
+        dout.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        t0 = 0
+        for s, m in enumerate(ns):
+            w = slice(t0, t0 + m)
+            want, _, tol, _ = R.attend(q[w], cache.rows("k", s, kv[s]), cache.rows("v", s, kv[s]), kv[s] - m, 0.125, True, 0)
+            R.assert_within(out[w], want, tol, f"attention of sequence {s}, {m} rows")
+            o, S1 = R.delta(*(t[w] for t in x), S[s], DK ** -0.5, True)
+            # outputs: as in check_delta; the state carries fp32's errors alone (three-term operands)
+            mag = S1.abs().amax()
+            R.assert_within(dout[w], o, R.U_BF16 * 1.01 * o.abs() + 2.0 ** -14 * mag, f"delta rule of sequence {s}")
+            R.assert_within(st.state[2 + s], S1, 32 * R.U_F32 * math.sqrt(DK + m) * mag * torch.ones_like(S1), f"state {s}")
+            t0 += m
+        assert (out[t0:] == 5.0).all() and (dout[t0:] == 5.0).all()
+    assert B.lmoe_last_device_status(ws) == B.LMOE_OK and B.lmoe_last_device_status(dws) == B.LMOE_OK
+
+
+def test_two_streams_with_a_workspace_each():
+    cache = R.Cache("int8", 2, 128, 16, [500])
+    pk = paged(cache, 20, 2, 128)
+    q = torch.randn(120, 20, 128, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    b = batch_of(pk, cache, [120])
+    want = pk.attend(q, b, pk.workspace())
+    streams, wss = [torch.cuda.Stream() for _ in range(2)], [pk.workspace() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(pk.attend(q, b, wss[i]))
+    torch.cuda.synchronize()
+    for g in got[0] + got[1]:
+        assert torch.equal(g.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_a_layers_steps(fmt):
+    """As a model runs them: a prompt in two chunks, then a verify window and single tokens, each appended and then
+    attended to; and the states of a delta layer carried through the same steps."""
+    Hq, Hk, D, page = 8, 2, 128, 32
+    g = torch.Generator().manual_seed(3)
+    lens = [0, 0]
+    total = 200
+    cache = R.Cache(fmt, Hk, D, page, [total, total], seed=4)
+    cache.table = cache.table.clone()
+    pk = paged(cache, Hq, Hk, D)
+    ws = pk.workspace()
+    H, DK = 4, 64
+    st = mixers.DeltaStates(H, 2, DK, DK, n_states=2, l2norm=True, device=DEV)
+    S = torch.zeros(2, H, DK, DK, dtype=torch.float64)
+    place = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    from_zero = torch.tensor([-1, -1], dtype=torch.int32, device=DEV)
+    for step, ns in enumerate(([100, 40], [33, 64], [4, 4], [1, 1], [1, 0])):
+        T = sum(ns)
+        lens = [a + n for a, n in zip(lens, ns)]
+        qkv = torch.randn(T, Hq + 2 * Hk, D, generator=g).bfloat16()
+        d = qkv.to(DEV)
+        b = batch_of(pk, cache, ns, lens=lens)
+        pk.append(d[:, Hq:Hq + Hk], d[:, Hq + Hk:], b, ws)
+        out = pk.attend(d[:, :Hq], b, ws)
+        back = pk.read(b, ws)
+        dws = st.workspace(T, 2, max(ns))
+        x = delta_inputs(T, H, 2, DK, DK, 10 + step, l2norm=True)
+        dout = st.forward(*(t.to(DEV) for t in x), st.batch(R.starts(ns).to(DEV), place if step else from_zero, place, T, max(ns)), dws)
+        t0 = 0
+        for s, n in enumerate(ns):
+            w = slice(t0, t0 + n)
+            for name, i in (("k", Hq), ("v", Hq + Hk)):
+                cache.put(name, s, range(lens[s] - n, lens[s]), qkv[w, i:i + Hk])
+            K, V = cache.rows("k", s, lens[s]), cache.rows("v", s, lens[s])
+            for y, want in zip(back, (K, V)):
+                if n:
+                    R.assert_within(y[w], want[lens[s] - n:], R.U_BF16 * want[lens[s] - n:].abs() * (1 + 2.0 ** -20), "read back")
+            if n:
+                want, _, tol, _ = R.attend(qkv[w, :Hq], K, V, lens[s] - n, D ** -0.5, True, 0)
+                R.assert_within(out[w], want, tol, f"step {step}, attention of sequence {s}")
+            o, S[s] = R.delta(*(t[w] for t in x), S[s], DK ** -0.5, True)
+            mag = S[s].abs().amax()
+            if n:
+                R.assert_within(dout[w], o, R.U_BF16 * 1.01 * o.abs() + 2.0 ** -14 * mag, f"step {step}, delta rule of sequence {s}")
+            # every step's errors are fp32 roundings of a sum that contracts
+            R.assert_within(st.state[s], S[s], 64 * R.U_F32 * math.sqrt(DK + lens[s]) * mag * torch.ones_like(S[s]), f"step {step}, state {s}")
+            t0 += n
+    assert B.lmoe_last_device_status(ws) == B.LMOE_OK
+
+
+@pytest.mark.parametrize("ns", [[1, 16], [300, 17, 64]])
+def test_delta_states_keep_fp32(ns):
+    """Operands of 16 bits would leave 2^-18 in the state; fp32's own steps leave a tenth of that."""
+    H, Hq, DK, DV = 4, 2, 128, 128
+    T = sum(ns)
+    x = delta_inputs(T, H, Hq, DK, DV, 21, l2norm=True)
+    S = torch.randn(len(ns), H, DK, DV, generator=torch.Generator().manual_seed(22))
+    st = mixers.DeltaStates(H, Hq, DK, DV, l2norm=True, state=S.to(DEV))
+    ws = st.workspace(T, len(ns), max(ns))
+    place = torch.arange(len(ns), dtype=torch.int32, device=DEV)
+    st.forward(*(t.to(DEV) for t in x), st.batch(R.starts(ns).to(DEV), place, place, T, max(ns)), ws)
+    t0 = 0
+    for s, n in enumerate(ns):
+        _, want = R.delta(*(t[t0:t0 + n] for t in x), S[s], DK ** -0.5, True)
+        got = st.state[s].double().cpu()
+        # relative error in the mean: sqrt(4 roundings of half a step a chunk, at most 10 chunks remembered) < 2^-20.7
+        assert (got - want).norm() / want.norm() < 2.0 ** -20.7
+        t0 += n
