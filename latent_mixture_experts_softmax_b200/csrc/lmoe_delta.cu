@@ -687,15 +687,16 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
 constexpr int kScanThreads = 160;           // four warps compute, the fifth loads
 constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (about 2 s)
 constexpr int kN = 32;                       // state columns of a block
+constexpr int kStages = 3;
 
 template <int DK>
 struct Scan {
     struct Stage {
         uint16_t k[kC][DK + 8], q[kC][DK + 8], v[kC][kN + 8];
         ChunkData d;
-    } st[2];
+    } st[kStages];
     float4 part[4][6][32];                   // a warp's share of K S and Q S for its partner
-    uint64_t full[2], empty[2];              // stages
+    uint64_t full[kStages], empty[kStages];
     uint64_t wrote[2], read[2];              // shares of the two warps of a group
     int abort;
 };
@@ -720,9 +721,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
     if (r.n < 0) return;
     const int n_chunks = chunks_of(r.n);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             sm100::mbar_init(&sm.full[i], 32);
             sm100::mbar_init(&sm.empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             sm100::mbar_init(&sm.wrote[i], 2);
             sm100::mbar_init(&sm.read[i], 2);
         }
@@ -735,10 +738,10 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
         sm100::grid_dep_wait();              // the chunks' data is written
         const ChunkData* data = reinterpret_cast<const ChunkData*>(p.chunk_ws) + ((size_t)base * p.H + h);
         int c = 0;
-        for (; c < n_chunks; ++c) {
-            const bool ok = sm100::mbar_wait(&sm.empty[c & 1], ((c >> 1) & 1) ^ 1, abort, kWaitLimit);
+        for (int st = 0, ph = 1; c < n_chunks; ++c, st = st + 1 < kStages ? st + 1 : 0, ph ^= st == 0) {
+            const bool ok = sm100::mbar_wait(&sm.empty[st], ph, abort, kWaitLimit);
             if (!__all_sync(0xffffffffu, ok)) break;
-            typename Scan<DK>::Stage& x = sm.st[c & 1];
+            typename Scan<DK>::Stage& x = sm.st[st];
             const int n_here = min(kC, r.n - c * kC);
             const size_t row0 = (size_t)r.q0 + (size_t)c * kC;
             rows_async<DK, DK + 8>(&x.k[0][0], p.k + row0 * p.ks + (size_t)hq * DK, p.ks, n_here, lane);
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int i = 0; i < kWhole; ++i) cp_async16(xd + 512 * i, d + 512 * i);
             if (lane < (int)(sizeof(ChunkData) % 512 / 16)) cp_async16(xd + 512 * kWhole, d + 512 * kWhole);
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(&sm.full[c & 1])) : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(&sm.full[st])) : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         return;
@@ -770,11 +773,11 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             for (int i = 0; i < 4; ++i) S[j][i] = src[(size_t)(8 * j + (i & 1)) * p.DV + 8 * (i >> 1)];
     }
     bool dead = false;
-    for (int c = 0; c < n_chunks; ++c) {
-        dead = !sm100::mbar_wait(&sm.full[c & 1], (c >> 1) & 1, abort, kWaitLimit);
+    for (int c = 0, st = 0, ph = 0; c < n_chunks; ++c, st = st + 1 < kStages ? st + 1 : 0, ph ^= st == 0) {
+        dead = !sm100::mbar_wait(&sm.full[st], ph, abort, kWaitLimit);
         dead = __any_sync(0xffffffffu, dead);
         if (dead) break;
-        const typename Scan<DK>::Stage& x = sm.st[c & 1];
+        const typename Scan<DK>::Stage& x = sm.st[st];
         // ---- this warp's share of (K S)^T and (Q S)^T: 16 columns x 32 tokens
         float ks[4][4], qs[4][4];
 #pragma unroll
@@ -946,7 +949,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
             for (int j = 0; j < 2; ++j) mma_bf16(o[j], lo, f[j].x, f[j].y);
         }
         __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&sm.empty[c & 1]);
+        if (lane == 0) sm100::mbar_arrive(&sm.empty[st]);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
