@@ -209,7 +209,6 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
     __shared__ __align__(16) uint16_t sk[kC][DK + 8], sq[kC][DK + 8];
     __shared__ __align__(16) float kk[kC][kC + 4], qk[kC][kC + 4], sa[2][kC][kC + 4];
     __shared__ float s_rk[kC], s_rq[kC], s_gh[4][kC], s_gl[4][kC];
-    sm100::grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int hq = blockIdx.y;
     for (int s = blockIdx.z; s < p.n_seqs; s += gridDim.z) {
@@ -297,7 +296,8 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                 for (int i = 0; i < kC; ++i) {                   // column `lane` of b_i D_ij (k_i k_j)
                     const float d = exp_of((xh[i] - gh) + (xl[i] - gl));
                     const float bi = __shfl_sync(0xffffffffu, br, i);
-                    m[i][lane] = lane < i ? kk[i][lane] * (bi * rk) * d : 0.f;
+                    const float y = kk[i][lane] * (bi * rk) * d;     // (every lane: a branch here waits for its load)
+                    m[i][lane] = lane < i ? y : 0.f;
                 }
                 __syncwarp();
                 // the inverse by blocks of 16: T11 and T22 a column a lane,
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                     for (int c = 0; c < 4; ++c) {
                         const int col = 16 * k + 2 * t + (c & 1) + 8 * (c >> 1);
                         const float d = exp_of((xh[i] - xh[col]) + (xl[i] - xl[col]));
-                        u[c] = col <= i ? qk[i][col] * (s_rq[i] * s_rk[col]) * d : 0.f;
+                        const float y = qk[i][col] * (s_rq[i] * s_rk[col]) * d;
+                        u[c] = col <= i ? y : 0.f;
                     }
                     uint4 x;
                     split2(u[0], u[1], x.x, x.z);
@@ -512,7 +513,8 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
 #pragma unroll
                 for (int i = 0; i < kFew; ++i) {             // column `tok` of b_i D_ij (k_i k_j)
                     const float bi = __shfl_sync(0xffffffffu, br, i);
-                    x[i] = tok < i ? kk[i][tok] * (bi * rk) * exp_of((xh[i] - gh) + (xl[i] - gl)) : 0.f;
+                    const float y = kk[i][tok] * (bi * rk) * exp_of((xh[i] - gh) + (xl[i] - gl));
+                    x[i] = tok < i ? y : 0.f;
                 }
                 __syncwarp();
                 if (lane < kFew)
@@ -567,7 +569,8 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
                     for (int c = 0; c < 4; ++c) {
                         const int col = 2 * t + (c & 1) + 8 * (c >> 1);
                         const float d = exp_of((xh[i] - xh[col]) + (xl[i] - xl[col]));
-                        u[c] = col <= i ? qk[i][col] * (s_rq[i] * s_rk[col]) * d : 0.f;
+                        const float y = qk[i][col] * (s_rq[i] * s_rk[col]) * d;
+                        u[c] = col <= i ? y : 0.f;
                     }
                     uint4 x;
                     split2(u[0], u[1], x.x, x.z);
@@ -735,7 +738,6 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
     __syncthreads();
     volatile int* abort = &sm.abort;
     if (warp == 4) {
-        sm100::grid_dep_wait();              // the chunks' data is written
         const ChunkData* data = reinterpret_cast<const ChunkData*>(p.chunk_ws) + ((size_t)base * p.H + h);
         int c = 0;
         for (int st = 0, ph = 1; c < n_chunks; ++c, st = st + 1 < kStages ? st + 1 : 0, ph ^= st == 0) {
@@ -987,17 +989,11 @@ cudaError_t run_chunks(const DeltaParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = allow_smem<k_delta_scan<DK>>(sizeof(Scan<DK>));
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((size_t)p.n_seqs * p.H * (p.DV / kN)));
-    cfg.blockDim = dim3(kScanThreads);
-    cfg.dynamicSmemBytes = sizeof(Scan<DK>);
-    cfg.stream = st;
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    a[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = a;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_delta_scan<DK>, p, slots);
+    // (Not overlapped with the chunks' kernel: blocks that start while it
+    // drains gather two to an SM on the first SMs to empty, which are then the
+    // last to finish: 394 us for one sequence of 4096 tokens instead of 275.)
+    k_delta_scan<DK><<<(unsigned)((size_t)p.n_seqs * p.H * (p.DV / kN)), kScanThreads, sizeof(Scan<DK>), st>>>(p, slots);
+    return cudaGetLastError();
 }
 
 }  // namespace
