@@ -62,22 +62,25 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 // few query rows
 // ---------------------------------------------------------------------------
 
-// D, code format, NR tiles of 8 query rows, NS warps that share a step (each
-// holding D / NS of the output columns, which bounds the accumulators to 128
-// registers).
+// D, code format, NR tiles of 8 query rows, NS warps that share a step: each
+// sums the scores over D / NS of the columns, which they add up through shared
+// memory, and holds D / NS of the output columns, which bounds the
+// accumulators to 128 registers.
 template <int D, int FMT, int NR, int NS>
 struct Few {
     static constexpr int kRows = 8 * NR;
     static constexpr int kGroups = kWarps / NS;
     static constexpr int kSteps = D / 16;              // K steps of the score product
-    static constexpr int kKw = D / 16;                 // words of a key row per lane (D / 4 bytes)
+    static constexpr int kOwn = kSteps / NS;           // those of a warp
+    static constexpr int kKw = kOwn;                   // words of a key row per lane
     static constexpr int kVw = D / 32 / NS;            // words of a value row per lane
     static constexpr int kTiles = 2 * kVw;             // M tiles of the output product per warp
     static constexpr int kOut = kTiles * 4 * NR;       // accumulators
-    static constexpr bool kQInRegs = kSteps * 2 * NR <= 32;
+    static constexpr bool kQInRegs = kOwn * 2 * NR <= 32;
     static constexpr size_t kQBytes = (size_t)kSteps * NR * 32 * 8;
     static constexpr size_t kJoinBytes = (size_t)(kGroups / 2) * NS * kOut * 32 * 4;
-    static constexpr size_t kSmem = kQBytes + kJoinBytes;
+    static constexpr size_t kShareBytes = NS == 2 ? (size_t)2 * kWarps * 4 * NR * 32 * 4 : 0;
+    static constexpr size_t kSmem = kQBytes + kJoinBytes + kShareBytes;
     static constexpr int kCtasPerSm = kOut <= 32 ? 2 : 1;   // 128 or 255 registers a thread
 };
 
@@ -88,6 +91,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
     extern __shared__ __align__(16) char smem[];
     uint2* qf = reinterpret_cast<uint2*>(smem);                       // query fragments [step][NR][lane]
     float* jbuf = reinterpret_cast<float*>(smem + C::kQBytes);
+    float4* share = reinterpret_cast<float4*>(smem + C::kQBytes + C::kJoinBytes);     // [2][warp][NR][lane]
     __shared__ float s_qscale[kMaxRows];
     __shared__ int s_pos[kMaxRows];
     __shared__ float s_m[kWarps][kMaxRows], s_l[kWarps][kMaxRows];
@@ -162,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
         __syncthreads();
 
         float qscale[NR][2];
-        uint2 q_reg[C::kQInRegs ? C::kSteps : 1][NR];
+        uint2 q_reg[C::kQInRegs ? C::kOwn : 1][NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             qscale[r][0] = s_qscale[8 * r + 2 * t];
             qscale[r][1] = s_qscale[8 * r + 2 * t + 1];
             if (C::kQInRegs) {
 #pragma unroll
-                for (int k = 0; k < C::kSteps; ++k) q_reg[k][r] = qf[((size_t)k * NR + r) * 32 + lane];
+                for (int k = 0; k < C::kOwn; ++k) q_reg[k][r] = qf[((size_t)(hs * C::kOwn + k) * NR + r) * 32 + lane];
             }
         }
 
@@ -208,9 +212,9 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
         auto load_k = [&](size_t base) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint8_t* src = p.k + (base + g + 8 * h) * D + t * 16;
+                const uint8_t* src = p.k + (base + g + 8 * h) * D + hs * (D / NS) + t * 16;
 #pragma unroll
-                for (int i = 0; i < D / 64; ++i) {
+                for (int i = 0; i < D / 64 / NS; ++i) {
                     const uint4 v = ldg_stream(reinterpret_cast<const uint4*>(src + i * 64));
                     kw[h][4 * i] = v.x;
                     kw[h][4 * i + 1] = v.y;
@@ -243,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
         };
         size_t row_next = 0;
         bool ok_next = false;
+        int odd = 0;
         if (st < st_end) {
             row = locate(st, ok);
             load_k(row);
@@ -258,15 +263,31 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[r][i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < C::kSteps; ++k) {
+            for (int k = 0; k < C::kOwn; ++k) {
                 uint32_t a[4];
                 codes_to_f16<FMT>(biased<FMT>(kw[0][k]), a[0], a[2]);
                 codes_to_f16<FMT>(biased<FMT>(kw[1][k]), a[1], a[3]);
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    const uint2 b = C::kQInRegs ? q_reg[C::kQInRegs ? k : 0][r] : qf[((size_t)k * NR + r) * 32 + lane];
+                    const uint2 b = C::kQInRegs ? q_reg[C::kQInRegs ? k : 0][r] : qf[((size_t)(hs * C::kOwn + k) * NR + r) * 32 + lane];
                     mma_f16(s[r], a, b.x, b.y);
                 }
+            }
+            if (NS == 2) {           // (both add the same two numbers; the next step uses the other half of the buffer)
+                float4* mine = share + (((size_t)odd * kWarps + warp) * NR) * 32 + lane;
+                const float4* other = share + (((size_t)odd * kWarps + (warp ^ 1)) * NR) * 32 + lane;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) mine[r * 32] = make_float4(s[r][0], s[r][1], s[r][2], s[r][3]);
+                named_bar_sync(1 + grp, 64);
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float4 y = other[r * 32];
+                    s[r][0] += y.x;
+                    s[r][1] += y.y;
+                    s[r][2] += y.z;
+                    s[r][3] += y.w;
+                }
+                odd ^= 1;
             }
             const float k0 = ks[0], k1 = ks[1];
             // scales that are no positive numbers make a score NaN (a row
