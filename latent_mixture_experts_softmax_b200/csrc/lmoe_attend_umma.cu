@@ -882,7 +882,9 @@ template <int D, int FMT>
 cudaError_t launch_groups(AttendParams p, cudaStream_t st) {
     const long long tiles = (((long long)p.table_stride << p.page_log2) + image_tokens(D) - 1) / image_tokens(D);
     const long long fit = (long long)(kImageBytes / image_bytes(D)) / tiles;      // (sequence, head) pairs of a group
-    if ((long long)p.max_new * p.G <= kImageRowTiles * many_rows(D) || fit < 1) return launch<D, FMT, false>(p, st);
+    const long long rows = (long long)p.max_new * p.G;
+    const bool brief = rows > many_rows(D) && tiles * image_tokens(D) <= kImageTokens && (long long)p.n_seqs * p.Hk <= fit;
+    if (fit < 1 || (rows <= kImageRowTiles * many_rows(D) && !brief)) return launch<D, FMT, false>(p, st);
     const int heads = (int)(fit < p.Hk ? fit : p.Hk);
     const int seqs = (int)(fit / heads < p.n_seqs ? fit / heads : p.n_seqs);
     AttendParams g = p;
