@@ -10,10 +10,13 @@
 // Folding the value's scale into the exponent keeps the second product in
 // fp16 whatever the scales are: p is below 2^16 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
-// that of p to fp16 (half a step, 2^-12).  Queries are scaled by a power of
+// that of p to fp16 (half a step, 2^-11).  Queries are scaled by a power of
 // two per row into the fp16 range, which is exact; sums are fp32.
 //
-// What bounds it: the bytes of the codes, each read once.  The products run
+// What bounds it: the bytes of the codes, each read once (64 tokens of a batch
+// over up to 16K cached ones: 131 us, 4.4 TB/s), up to 8 rows; with 32 rows
+// and head_dim 256 the latency of one block of eight warps an SM (32 tokens
+// over up to 128K: 258 us, 2.4 TB/s).  The products run
 // on mma.sync m16n8k16 with the tokens as M (S^T = K Q^T) and the query rows
 // as N, so 8 rows cost one instruction per 16 tokens and 16 columns, and
 // neither product needs a transposed copy of the codes: both sums run over

@@ -3,8 +3,14 @@
 //
 // The mathematics is that of the kernel for few rows (lmoe_attend.cu); the
 // products run on tcgen05 (kind::f16, fp32 accumulators in tensor memory).
-// What bounds it: the tensor cores (4 D flops per row and key) and, close
-// behind, the exponentials (one per row and key, 16 a cycle and SM).
+// What bounds it: shared memory.  A tile of 64 tokens and 256 rows of
+// head_dim 128 takes the tensor core 1024 cycles of operands (Q and K for S,
+// V for O; the products alone take as long), 256 of incoming tiles, and about
+// 1200 of the tokens' constants (three floats a token and row, broadcast at
+// 0.8 cycles each); the exponentials, 16 a cycle and SM, take 1024 beside
+// them.  Measured: about 2900 cycles a tile; 4096 causal tokens of 20 heads
+// in 159 us (540 TFLOP/s), 2048 tokens over 32768 of head_dim 256 in 730 us
+// (910 TFLOP/s).
 //
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
@@ -14,21 +20,18 @@
 //                tile each; where there is one tile, they take its key tiles in
 //                turn, handing on the row's reference.  (Warps that meet in
 //                every tile do the exponentials at the same time, and the units
-//                for those stand still in between: 2600 cycles a tile of 256
-//                rows.)
-//   keys, values four warps each read the codes of a tile (registers, one tile
-//                ahead) and write them as fp16 operands with the 128-byte
-//                swizzle; a key row is K-major as it is stored, and the same
-//                layout read as MN-major is the value operand, so neither is
-//                transposed.
-//   issue        one thread: S = Q K^T and O += P V
-// Two score buffers per query tile let the next S run ahead of the softmax.  The row's
+//                for those stand still in between.)
+//   keys, values the operands of a tile: a key row is K-major as it is stored,
+//                and the same layout read as MN-major is the value operand, so
+//                neither is transposed.  One thread each fetches them as images
+//                (k_attend_images) that were laid out once for all row tiles;
+//                where few row tiles read a key tile (launch_groups), four
+//                warps each read the codes (registers, a tile ahead) and write
+//                them as fp16 with the 128-byte swizzle.
+//   issue        one warp: S = Q K^T and O += P V
+// Four score buffers let S run two tiles ahead of the sums.  The row's
 // reference m is raised as in the kernel for few rows, and to a whole number,
-// so that what it rescales (O, and the P of the tile's earlier pieces)
-// changes by a power of two: the scores are gone
-// through once, and the loop stays small enough for the instruction caches
-// (a form that held a tile's scores in registers, unrolled, spent a third of
-// its time waiting for instructions).
+// so that what it rescales changes by a power of two.
 //
 // Work is cut into equal pieces of the line of (item, key tile) units as in
 // the kernel for few rows, one piece per CTA; cut items are joined after it.
