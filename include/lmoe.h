@@ -367,8 +367,9 @@ typedef struct {
 LMOE_API int lmoe_attn_cfg_check(const lmoe_attn_cfg* cfg);
 
 /* Bytes of the workspace of lmoe_kv_append, lmoe_kv_read and lmoe_attend for
- * batches of any size (the lengths do not enter).  0 if the configuration
- * is unsupported. */
+ * batches of any size (the lengths do not enter): 64 MiB and some, most of it
+ * for the operands of lmoe_attend's prompt chunks.  0 if the configuration is
+ * unsupported. */
 LMOE_API size_t lmoe_attn_workspace_bytes(const lmoe_attn_cfg* cfg);
 
 /* Quantise the new tokens' keys and values into the cache.
@@ -404,8 +405,9 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  * fp16.  The scales of the value rows that one query sees may lie up to
  * 2^100 apart.  Results do not depend on timing.
  * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that
- * is not finite), _UNSUPPORTED, _WORKSPACE; n_tokens = 0 or n_seqs = 0
- * launches nothing. */
+ * is not finite), _UNSUPPORTED (also 2^31 - 1024 or more query rows of one
+ * sequence and key head), _WORKSPACE; n_tokens = 0 or n_seqs = 0 launches
+ * nothing. */
 LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_kv_batch* batch, const void* q,
                          size_t q_stride, float softmax_scale, int causal, int window, void* out, float* lse, void* ws,
                          size_t ws_bytes, void* stream);
@@ -455,8 +457,8 @@ LMOE_API size_t lmoe_delta_workspace_bytes(const lmoe_delta_cfg* cfg, int n_toke
  * A sequence without new tokens copies its state.  Checked on the device
  * (LMOE_ERR_DEVICE_CHECK, the sequence is left out): rows as in
  * lmoe_kv_batch, src or dst outside [-1, n_states).
- * Errors: LMOE_ERR_ARG, _UNSUPPORTED, _WORKSPACE; n_seqs = 0 launches
- * nothing. */
+ * Errors: LMOE_ERR_ARG, _UNSUPPORTED (also n_seqs * n_heads * head_v / 32
+ * beyond 2^31 - 1), _WORKSPACE; n_seqs = 0 launches nothing. */
 LMOE_API int lmoe_delta_rule(const lmoe_delta_cfg* cfg, const lmoe_delta_batch* batch, const void* q, const void* k,
                              const void* v, size_t q_stride, size_t k_stride, size_t v_stride, const float* log_decay,
                              const float* beta, float scale, float* states, void* out, void* ws, size_t ws_bytes,

@@ -62,7 +62,9 @@ int kv_params(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_k
     p->n_seqs = b->n_seqs;
     p->table_stride = b->pages_per_seq;
     p->n_tokens = b->n_tokens;
-    p->max_new = b->max_new;
+    p->max_new = b->max_new < b->n_tokens ? b->max_new : b->n_tokens;
+    // query rows of a sequence and key head are counted in an int
+    if ((long long)p->max_new * p->G > 0x7fffffff - 1024) return LMOE_ERR_UNSUPPORTED;
     p->ctrl = static_cast<Ctrl*>(ws);
     return LMOE_OK;
 }
@@ -160,6 +162,7 @@ int lmoe_delta_rule(const lmoe_delta_cfg* cfg, const lmoe_delta_batch* b, const 
         if (!log_decay || !beta || !out || !aligned(log_decay, 4) || !aligned(beta, 4) || !aligned(out, 16))
             return LMOE_ERR_ARG;
     }
+    if ((long long)b->n_seqs * cfg->n_heads * (cfg->head_v / 32) > 0x7fffffff) return LMOE_ERR_UNSUPPORTED;   // blocks of a launch
     if (!ws || !aligned(ws, 256)) return LMOE_ERR_ARG;
     if (ws_bytes < delta_ws(*cfg, b->n_tokens, b->n_seqs, b->max_new)) return LMOE_ERR_WORKSPACE;
     DeltaParams p;
@@ -176,7 +179,7 @@ int lmoe_delta_rule(const lmoe_delta_cfg* cfg, const lmoe_delta_batch* b, const 
     p.n_seqs = b->n_seqs;
     p.n_states = b->n_states;
     p.n_tokens = b->n_tokens;
-    p.max_new = b->max_new;
+    p.max_new = b->max_new < b->n_tokens ? b->max_new : b->n_tokens;
     p.q = static_cast<const uint16_t*>(q);
     p.k = static_cast<const uint16_t*>(k);
     p.v = static_cast<const uint16_t*>(v);

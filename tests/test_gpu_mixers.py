@@ -610,3 +610,9 @@ def test_delta_states_keep_fp32(ns):
         # relative error in the mean: sqrt(4 roundings of half a step a chunk, at most 10 chunks remembered) < 2^-20.7
         assert (got - want).norm() / want.norm() < 2.0 ** -20.7
         t0 += n
+
+
+def test_a_loose_bound_of_new_tokens():
+    """max_new far above what any sequence has (a program that does not count) costs no more than n_tokens does."""
+    check_delta(2, 1, 64, 64, [40, 3], True, max_new=1 << 30)
+    check_attend("int8", 4, 2, 64, 16, [40, 3], [90, 3], max_new=1 << 30)

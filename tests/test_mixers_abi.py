@@ -91,6 +91,16 @@ def test_delta_refusals(L):
     assert go(batch=B.lmoe_delta_batch(None, None, None, 0, 4, 6, 3), ws=None) == B.LMOE_OK
 
 
+def test_sizes_that_no_launch_can_count_are_refused(L):
+    cfg = B.lmoe_attn_cfg(8, 2, 64, 16, 0)
+    many = B.lmoe_kv_batch(256, 256, 256, 1, 4, 2 ** 30, 2 ** 30)
+    cache = B.lmoe_kv_cache(256, 256, 256, 256, 4)
+    assert L.lmoe_attend(cfg, cache, many, 256, 512, 1.0, 1, 0, 256, None, 256, 1 << 40, None) == B.LMOE_ERR_UNSUPPORTED
+    cfg = B.lmoe_delta_cfg(4, 2, 64, 64, 0)
+    many = B.lmoe_delta_batch(256, 256, 256, 2 ** 30, 4, 6, 3)
+    assert L.lmoe_delta_rule(cfg, many, 256, 256, 256, 128, 128, 256, 256, 256, 1.0, 256, 256, 256, 1 << 40, None) == B.LMOE_ERR_UNSUPPORTED
+
+
 def test_the_structures_have_the_headers_layout():
     for c, fields in ((B.lmoe_kv_cache, 4 * 8 + 8), (B.lmoe_kv_batch, 3 * 8 + 16), (B.lmoe_delta_batch, 3 * 8 + 16),
                       (B.lmoe_attn_cfg, 20), (B.lmoe_delta_cfg, 20)):
