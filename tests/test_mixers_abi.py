@@ -1,6 +1,7 @@
 """Host side of the token mixers: shapes, sizes and refusals, without a GPU."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -99,6 +100,30 @@ def test_sizes_that_no_launch_can_count_are_refused(L):
     cfg = B.lmoe_delta_cfg(4, 2, 64, 64, 0)
     many = B.lmoe_delta_batch(256, 256, 256, 2 ** 30, 4, 6, 3)
     assert L.lmoe_delta_rule(cfg, many, 256, 256, 256, 128, 128, 256, 256, 256, 1.0, 256, 256, 256, 1 << 40, None) == B.LMOE_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("top", [127, 448])
+def test_codes_by_reciprocals_are_those_of_exact_quotients(top):
+    """The rule of the cache's write kernel (the product with the rounded reciprocal, to 20 bits, then to the codes'
+    grid) in fp32, over every pair of bf16 significands and every shift that leaves a code, against integers."""
+    X = np.arange(256, dtype=np.int64)
+    for A in range(128, 256):
+        inv = np.float32(1) / np.float32(A)
+        for sh in range(20):
+            x = X[X <= A << sh]
+            y = (x.astype(np.float32) * np.float32(2.0 ** -sh) * np.float32(top)) * inv
+            y = ((y.view(np.uint32) + np.uint32(8)) & np.uint32(0xFFFFFFF0)).view(np.float32).astype(np.float64)
+            num, den = x * top, np.int64(A) << sh               # the quotient
+            # the codes' steps: 1, or 2^(e - 3) in the binade e from -6 on (the largest power of two at most num / den)
+            e = np.zeros_like(x) + 3 if top == 127 else np.full_like(x, -6)
+            if top == 448:
+                for i in range(-5, 9):
+                    e[num * 2 ** max(0, -i) >= den * 2 ** max(0, i)] = i
+            up, down = 2 ** np.maximum(0, 3 - e), 2 ** np.maximum(0, e - 3)
+            k, r = np.divmod(num * up, den * down)
+            k += (2 * r > den * down) | ((2 * r == den * down) & (k % 2 == 1))
+            step = 2.0 ** (e - 3)
+            assert np.array_equal(np.rint(y / step), k.astype(np.float64)), (A, sh)
 
 
 def test_the_structures_have_the_headers_layout():
