@@ -3,14 +3,14 @@
 //
 // The mathematics is that of the kernel for few rows (lmoe_attend.cu); the
 // products run on tcgen05 (kind::f16, fp32 accumulators in tensor memory).
-// What bounds it: shared memory.  A tile of 64 tokens and 256 rows of
-// head_dim 128 takes the tensor core 1024 cycles of operands (Q and K for S,
-// V for O; the products alone take as long), 256 of incoming tiles, and about
-// 1200 of the tokens' constants (three floats a token and row, broadcast at
-// 0.8 cycles each); the exponentials, 16 a cycle and SM, take 1024 beside
-// them.  Measured: about 2900 cycles a tile; 4096 causal tokens of 20 heads
-// in 159 us (540 TFLOP/s), 2048 tokens over 32768 of head_dim 256 in 730 us
-// (910 TFLOP/s).
+// What bounds it: the softmax warps' own chain.  Of about 2900 cycles a tile of
+// 64 tokens and 256 rows (head_dim 128), a warp takes 640 to scale its scores,
+// 780 for the exponentials and sums (two warps of a scheduler share 1024 of
+// the exponential unit), 300 for votes and the rare change of the reference,
+// and the rest waits for barriers; the tensor core needs 1024, at the pace at
+// which shared memory gives it Q, K and V.  4096 causal tokens of 20 heads take
+// 157 us (546 TFLOP/s), 2048 tokens over 32768 of head_dim 256 715 us (930
+// TFLOP/s; the card runs that power-capped).
 //
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
 // (two for head_dim 64 and 128, one for 256) and walks the keys in tiles of
@@ -28,7 +28,8 @@
 //                where few row tiles read a key tile (launch_groups), four
 //                warps each read the codes (registers, a tile ahead) and write
 //                them as fp16 with the 128-byte swizzle.
-//   issue        one warp: S = Q K^T and O += P V
+//   issue        a warp per query tile: S = Q K^T and O += P V (one warp for both
+//                would make each wait for the other's probabilities)
 // Four score buffers let S run two tiles ahead of the sums.  The row's
 // reference m is raised as in the kernel for few rows, and to a whole number,
 // so that what it rescales changes by a power of two.
@@ -58,7 +59,7 @@ struct Many {
     static constexpr int kRows = NQ * 128;
     static constexpr int kKeyWarp = 8, kValueWarp = kKeyWarp + (IMG ? 1 : 4),
                          kMmaWarp = kValueWarp + (IMG ? 1 : 4);
-    static constexpr int kThreads = (kMmaWarp + 1) * 32;
+    static constexpr int kThreads = (kMmaWarp + NQ) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
     static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
@@ -209,8 +210,8 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
         for (int i = 0; i < 4; ++i) {
             mbar_init(&k_full[i], IMG ? 1 : 4);
             mbar_init(&v_full[i], IMG ? 1 : 4);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&k_empty[i], NQ);
+            mbar_init(&v_empty[i], NQ);
             mbar_init(&sc_full[i], IMG ? 1 : 4);
             mbar_init(&sc_free[i], CH ? 4 : 8);
             mbar_init(&s_full[i], 1);
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             mbar_init(&chain[i], 1);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], CH ? 8 : 4);
-        mbar_init(final_bar, 1);
+        mbar_init(final_bar, NQ);
         *abort_flag = 0;
         p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
         fence_barrier_init();
@@ -711,74 +712,64 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             const uint32_t idesc_s = idesc_f16(128, TK, 0), idesc_o = idesc_f16(128, D, 0) | kTransposeB;
             const uint64_t q_desc = sdesc_k128(smem_u32(sq)), k_desc = sdesc_k128(smem_u32(sk)),
                            v_desc = sdesc_mn128(smem_u32(sv), TK * 128);
-            auto scores = [&](int q, int b, int st) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + (NB * q + b) * TK, q_desc + ((q * C::kQBytes + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                           k_desc + ((st * C::kOpBytes + (k >> 2) * (TK * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0);
-            };
-            auto sums = [&](int q, int b, int st, bool first) {
-#pragma unroll
-                for (int k = 0; k < TK / 16; ++k)
-                    mma_ts(tmem + C::kColO + q * D, tmem + (NB * q + b) * TK + k * 8,
-                           v_desc + ((st * C::kOpBytes + k * 2048) >> 4), idesc_o, !first || k > 0);
-            };
+            const int q = warp - C::kMmaWarp;
+            const uint32_t tS = tmem + NB * q * TK, tO = tmem + C::kColO + q * D;
             auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-            uint32_t n = 0, ns[2] = {0, 0}, np[2] = {0, 0}, qc[2] = {0, 0};   // tiles, and per query tile
-            bool ok = true, issued = false;
+            uint32_t n = 0, ns = 0, np = 0, items = 0;       // tiles of the CTA, scores and sums issued, items
+            bool ok = true;
+            auto score = [&](uint32_t k) {
+                const int st = k & (NST - 1), b = ns & (NB - 1);
+                ok = wait_all(&k_full[st], k >> kStLog2);
+                if (!ok) return;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    mma_ss(tS + b * TK, q_desc + ((q * C::kQBytes + (i >> 2) * (128 * 128) + (i & 3) * 32) >> 4),
+                           k_desc + ((st * C::kOpBytes + (i >> 2) * (TK * 128) + (i & 3) * 32) >> 4), idesc_s, i > 0);
+                commit(&s_full[NB * q + b]);
+                commit(&k_empty[st]);
+                ++ns;
+            };
             while (more && ok) {
-                const int J = w.t1 - w.t0, nq = w.n_rows > 128 ? NQ : 1;
-                if (J > 0) {
-                    for (int q = 0; q < nq && ok; ++q) ok = wait_all(&q_full[q], qc[q]++);
+                const int J = w.t1 - w.t0;
+                if (q * 128 >= w.n_rows) {               // no rows: lets the stages go as they come
+                    for (int j = 0; j < J && ok; ++j, ++n) {
+                        const int st = n & (NST - 1);
+                        ok = wait_all(&k_full[st], n >> kStLog2) && wait_all(&v_full[st], n >> kStLog2);
+                        if (ok && lane == 0) {
+                            mbar_arrive(&k_empty[st]);
+                            mbar_arrive(&v_empty[st]);
+                        }
+                    }
+                } else if (J > 0) {
+                    ok = wait_all(&q_full[q], items++);
                     // scores run two tiles ahead of the sums.  Two buffers: those of tile j + 2 follow the sums of
                     // tile j, whose P their buffer held; four: they go before them
                     for (int j = -2; j < J && ok; ++j) {
                         const bool ahead = j + 2 < J;
                         const uint32_t k = n + (j < 0 ? j + 2 : 2);
-                        const int st = n & (NST - 1), st2 = k & (NST - 1);
-                        auto score = [&](int q) {
-                            if (q == 0) ok = wait_all(&k_full[st2], k >> kStLog2);
-                            if (!ok) return;
-                            tc_fence_after();
-                            issued = true;
-                            const int b = ns[q]++ & (NB - 1);
-                            scores(q, b, st2);
-                            commit(&s_full[NB * q + b]);
-                        };
-                        if (NB == 4 && ahead) {
-                            score(0);
-                            if (ok) commit(&k_empty[st2]);
-                        }
-                        if (j >= 0 && ok) ok = wait_all(&v_full[st], n >> kStLog2);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            if (q < nq && ok) {
-                                if (j >= 0) {
-                                    const int b = np[q] & (NB - 1);
-                                    ok = wait_all(&p_full[NB * q + b], np[q]++ >> kBufLog2);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                    sums(q, b, st, j == 0);
-                                    commit(&o_done[NB * q + b]);
-                                }
-                                if (NB == 2 && ahead) score(q);
-                            }
+                        if (ahead && (NB == 4 || j < 0)) score(k);
+                        if (j < 0 || !ok) continue;
+                        const int st = n & (NST - 1), b = np & (NB - 1);
+                        ok = wait_all(&v_full[st], n >> kStLog2) && wait_all(&p_full[NB * q + b], np >> kBufLog2);
                         if (!ok) break;
-                        if (NB == 2 && ahead) commit(&k_empty[st2]);
-                        if (j >= 0) {
-                            commit(&v_empty[st]);
-                            ++n;
-                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < TK / 16; ++i)
+                            mma_ts(tO, tS + b * TK + i * 8, v_desc + ((st * C::kOpBytes + i * 2048) >> 4), idesc_o, j > 0 || i > 0);
+                        commit(&o_done[NB * q + b]);
+                        commit(&v_empty[st]);
+                        ++np;
+                        if (ahead && NB == 2) score(k);
+                        ++n;
                     }
                 }
                 if (ok) more = w.next(p, pl);
             }
-            if (issued) {
-                // every MMA done before tensor memory is freed, even after an abort
-                commit(final_bar);
-                volatile int no_abort = 0;
-                mbar_wait(final_bar, 0, &no_abort, kWaitLimit);
-            }
+            // every MMA done before tensor memory is freed, even after an abort
+            commit(final_bar);
+            volatile int no_abort = 0;
+            mbar_wait(final_bar, 0, &no_abort, kWaitLimit);
         }
         __syncwarp();
     }
