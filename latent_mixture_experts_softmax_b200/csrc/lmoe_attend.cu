@@ -506,62 +506,106 @@ constexpr int kJoinThreads = 128;
 
 // Block (c, b): rows of the item that CTA c began and others went on with.
 // FEW: one row a block, whose four warps take parts in turn (an item of few
-// rows may be spread over all CTAs); else four rows a warp, one after the
-// other (an item of many rows has few parts).  Parts are added in a fixed
-// order.
+// rows may be spread over all CTAs); else four rows a warp side by side (an
+// item of many rows has few parts).  A lane looks at a part's reference and
+// sum, so that one load's time covers them all (one part after the other, a
+// prompt's join took 19 us).  Parts are added in a fixed order.
 template <int D, bool FEW>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, int rows) {
-    constexpr int kParts = FEW ? 4 : 1;         // warps that share a row's parts
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, RW = FEW ? 1 : 4, PS = FEW ? 4 : 1;   // rows of a warp, warps that share their parts
     __shared__ float s_o[FEW ? 4 : 1][FEW ? D : 1];
-    __shared__ float s_l[4], s_m[4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     grid_dep_wait();
     const int4 cut = p.cuts[blockIdx.x];
     if (cut.x < 0) return;
-    const int c = blockIdx.x, last = cut.w;
+    const int c = blockIdx.x, np = cut.w - c + 1;
     const SeqRows sr = seq_rows(p, cut.x);
     const int r0 = cut.z * rows, n_rows = min(rows, sr.n * p.G - r0);
+    const int rr0 = FEW ? blockIdx.y : blockIdx.y * 16 + warp * 4;
+    if (rr0 >= n_rows) return;                  // a whole block (FEW), or the warp's rows
     const size_t pf = part_floats(rows, D);
-    auto part = [&](int k) { return p.part + ((size_t)k * 2 + (k == c ? 1 : 0)) * pf; };
-    for (int i = 0; i < (FEW ? 1 : 4); ++i) {
-        const int rr = FEW ? blockIdx.y : blockIdx.y * 16 + warp * 4 + i;
-        if (rr >= n_rows) return;               // a whole block (FEW), or the warp's last rows
-        const int first = FEW ? warp : 0;
-        float m = -INFINITY;
-        for (int k = c + first; k <= last; k += kParts) m = fmaxf(m, part(k)[(size_t)rows * D + rr]);
-        if (FEW) {
-            if (lane == 0) s_m[warp] = m;
-            __syncthreads();
-            m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    auto part = [&](int k) { return p.part + ((size_t)(c + k) * 2 + (k == 0 ? 1 : 0)) * pf; };
+    int rr[RW];                                 // (past the last row: that row again)
+    float m[RW], l[RW], o[RW][V];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        rr[i] = min(rr0 + i, n_rows - 1);
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[i][v] = 0.f;
+    }
+    // (FEW: a warp's first two parts are on their way before the references
+    // are known: a single token's join is nothing but such waits)
+    float ahead[FEW ? 2 : 1][V];
+    if (FEW) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float* s = part(min(warp + PS * u, np - 1)) + (size_t)rr[0] * D + lane;
+#pragma unroll
+            for (int v = 0; v < V; ++v) ahead[u][v] = s[32 * v];
         }
-        const float mm = m == -INFINITY ? 0.f : m;
-        float o[V], l = 0.f;
+    }
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        const float* q = part(min(k0 + lane, np - 1)) + (size_t)rows * D;
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = 0.f;
-        for (int k = c + first; k <= last; k += kParts) {
-            const float* q = part(k);
-            const float f = ex2(q[(size_t)rows * D + rr] - mm);
-            l = fmaf(f, q[(size_t)rows * (D + 1) + rr], l);
+        for (int i = 0; i < RW; ++i) m[i] = fmaxf(m[i], q[rr[i]]);
+    }
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = fmaf(f, q[(size_t)rr * D + lane + 32 * v], o[v]);
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        const float* q = part(min(k0 + lane, np - 1)) + (size_t)rows * D;
+        float f[RW];
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+            const float x = ex2(q[rr[i]] - (m[i] == -INFINITY ? 0.f : m[i]));
+            f[i] = k0 + lane < np ? x : 0.f;
+            const float y = q[rows + rr[i]];
+            l[i] = k0 + lane < np ? fmaf(f[i], y, l[i]) : l[i];
         }
-        if (FEW) {
+        const int n = min(32, np - k0);
+        int j = FEW ? warp : 0;
+        if (FEW && k0 == 0) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = o[v];
-            if (lane == 0) s_l[warp] = l;
-            __syncthreads();
-            if (warp) return;
-            l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+            for (int u = 0; u < 2; ++u, j += PS) {
+                const float w = __shfl_sync(0xffffffffu, f[0], j);       // (0 past the last part)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                o[v] = s_o[0][lane + 32 * v] + s_o[1][lane + 32 * v] + s_o[2][lane + 32 * v] + s_o[3][lane + 32 * v];
+                for (int v = 0; v < V; ++v) o[0][v] = j < np ? fmaf(w, ahead[u][v], o[0][v]) : o[0][v];
+            }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t orow = (size_t)(sr.q0 + (r0 + rr) / p.G) * p.Hq + cut.y * p.G + (r0 + rr) % p.G;
+#pragma unroll 2
+        for (; j < n; j += PS) {
+            const float* s = part(k0 + j);
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.out[orow * D + lane + 32 * v] = f32_to_bf16_bits(o[v] * inv);
-        if (lane == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            for (int i = 0; i < RW; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f[i], j);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[i][v] = fmaf(w, s[(size_t)rr[i] * D + lane + 32 * v], o[i][v]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    if (FEW) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_o[warp][lane + 32 * v] = o[0][v];
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            o[0][v] = (s_o[0][lane + 32 * v] + s_o[1][lane + 32 * v]) + (s_o[2][lane + 32 * v] + s_o[3][lane + 32 * v]);
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const size_t orow = (size_t)(sr.q0 + (r0 + rr[i]) / p.G) * p.Hq + cut.y * p.G + (r0 + rr[i]) % p.G;
+#pragma unroll
+        for (int v = 0; v < V; ++v) p.out[orow * D + lane + 32 * v] = f32_to_bf16_bits(o[i][v] * inv);
+        if (lane == 0 && p.lse) p.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
     }
 }
 

@@ -9,7 +9,7 @@
 // the exponential unit), 300 for votes and the rare change of the reference,
 // and the rest waits for barriers; the tensor core needs 1024, at the pace at
 // which shared memory gives it Q, K and V.  4096 causal tokens of 20 heads take
-// 157 us (546 TFLOP/s), 2048 tokens over 32768 of head_dim 256 710 us (940
+// 154 us (557 TFLOP/s), 2048 tokens over 32768 of head_dim 256 712 us (935
 // TFLOP/s; the card runs that power-capped).
 //
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
