@@ -38,7 +38,7 @@ __device__ __forceinline__ Tile tile_of(const AttendParams& p, const Plan& pl, c
     int lo = 0, hi = s.kv;
     if (p.causal) {
         hi = min(hi, first + (r1 - 1) / p.G + 1);
-        if (p.window) lo = max(0, first + r0 / p.G - p.window + 1);
+        if (p.window) lo = (int)max(0ll, (long long)first + r0 / p.G - p.window + 1);
     }
     hi = max(hi, lo);
     Tile t;

@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(256) k_attend_images(AttendParams p) {
     sm100::grid_dep_launch();
     const SeqRows r = seq_rows(p, blockIdx.z);
     if (r.n <= 0) return;
-    const int first = r.kv - r.n, lo = p.window ? max(0, first - p.window + 1) : 0;
+    const int first = r.kv - r.n, lo = p.window ? (int)max(0ll, (long long)first - p.window + 1) : 0;
     const int tok0 = blockIdx.x * TK;
     if (tok0 >= r.kv || tok0 + TK <= lo) return;
     const int head = p.h0 + blockIdx.y;

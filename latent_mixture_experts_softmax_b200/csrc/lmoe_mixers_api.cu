@@ -132,7 +132,8 @@ int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe
     p.q_stride = q_stride;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.causal = causal != 0;
-    p.window = window;
+    // a window as wide as the cache hides nothing (and position - window stays in an int)
+    p.window = window < ((long long)p.table_stride << p.page_log2) ? window : 0;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     return cuda_status(run_attend(p, static_cast<char*>(ws) + kAttnCtrlBytes, static_cast<cudaStream_t>(stream)));
