@@ -403,7 +403,9 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  * Products are of the bf16 queries and the stored codes as fp16, exact, with
  * fp32 sums; the probabilities (times the value's scale) are rounded to
  * fp16.  The scales of the value rows that one query sees may lie up to
- * 2^100 apart.  Results do not depend on timing.
+ * 2^100 apart; those from 2^-109 (the smallest that lmoe_kv_append stores) to
+ * 2^109 leave 24 bits in the sum of exponentials, larger ones 12 or more.
+ * Results do not depend on timing.
  * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that
  * is not finite), _UNSUPPORTED (also 2^31 - 1024 or more query rows of one
  * sequence and key head), _WORKSPACE; n_tokens = 0 or n_seqs = 0 launches

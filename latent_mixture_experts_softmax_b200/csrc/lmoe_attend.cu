@@ -6,7 +6,8 @@
 // query head of its group); with codes c_j and scales a_j (keys), b_j
 // (values),
 //   t_j = scale log2(e) a_j (q . ck_j) + log2(b_j),   p_j = 2^(t_j - m),
-//   out = sum_j p_j cv_j / sum_j p_j (1 / b_j).
+//   out = sum_j p_j cv_j / sum_j p_j (1 / b_j)
+// (the second sum in a unit that keeps it inside fp32, kSumUnit).
 // Folding the value's scale into the exponent keeps the second product in
 // fp16 whatever the scales are: p is below 2^16 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
             const bool f0 = vs[0] > 0.f && vs[0] < INFINITY, f1 = vs[1] > 0.f && vs[1] < INFINITY;
             const float lv0 = f0 ? __log2f(vs[0]) : __int_as_float(0x7fffffff);
             const float lv1 = f1 ? __log2f(vs[1]) : __int_as_float(0x7fffffff);
-            const float iv0 = f0 ? __frcp_rn(vs[0]) : 1.f, iv1 = f1 ? __frcp_rn(vs[1]) : 1.f;
+            const float iv0 = f0 ? __frcp_rn(vs[0]) * kSumUnit : 1.f, iv1 = f1 ? __frcp_rn(vs[1]) * kSumUnit : 1.f;
             const int tok = st << 4;
             const bool whole = ok && tok + 15 <= min(pos_lo, it.rows.kv - 1) && tok > win_lo;
             const bool ok_now = ok;
@@ -463,13 +464,14 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                 for (int i = 0; i < 2; ++i) {
                     const int rr = 8 * r + 2 * t + i;
                     if (rr >= n_rows) continue;
-                    const float inv = cut ? 1.f : ltot[r][i] == 0.f ? 0.f : 1.f / ltot[r][i];
+                    const Norm norm = cut ? Norm{1.f, 1.f} : norm_of(ltot[r][i]);
                     const size_t orow = (size_t)(it.rows.q0 + (r0 + rr) / p.G) * p.Hq + it.head * p.G + (r0 + rr) % p.G;
 #pragma unroll
                     for (int w = 0; w < C::kVw; ++w) {
                         const int d = D == 64 ? g * 8 + 4 * w : ((hs + (w >> 2)) * 8 + g) * 16 + 4 * (w & 3);
-                        const float y[4] = {o[2 * w][r][i] * inv, o[2 * w][r][i + 2] * inv, o[2 * w + 1][r][i] * inv,
-                                            o[2 * w + 1][r][i + 2] * inv};
+                        float y[4] = {o[2 * w][r][i], o[2 * w][r][i + 2], o[2 * w + 1][r][i], o[2 * w + 1][r][i + 2]};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = y[e] * norm.inv * norm.post;
                         if (cut) {
                             *reinterpret_cast<float4*>(part + (size_t)rr * D + d) = make_float4(y[0], y[1], y[2], y[3]);
                         } else {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                             part[(size_t)C::kRows * D + rr] = mtot[r][i];
                             part[(size_t)C::kRows * (D + 1) + rr] = ltot[r][i];
                         } else if (p.lse) {
-                            p.lse[orow] = ltot[r][i] == 0.f ? -INFINITY : (mtot[r][i] + log2f(ltot[r][i])) * 0.6931471805599453f;
+                            p.lse[orow] = lse_of(mtot[r][i], ltot[r][i]);
                         }
                     }
                 }
@@ -601,11 +603,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, in
     }
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const Norm norm = norm_of(l[i]);
         const size_t orow = (size_t)(sr.q0 + (r0 + rr[i]) / p.G) * p.Hq + cut.y * p.G + (r0 + rr[i]) % p.G;
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.out[orow * D + lane + 32 * v] = f32_to_bf16_bits(o[i][v] * inv);
-        if (lane == 0 && p.lse) p.lse[orow] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+        for (int v = 0; v < V; ++v) p.out[orow * D + lane + 32 * v] = f32_to_bf16_bits(o[i][v] * norm.inv * norm.post);
+        if (lane == 0 && p.lse) p.lse[orow] = lse_of(m[i], l[i]);
     }
 }
 

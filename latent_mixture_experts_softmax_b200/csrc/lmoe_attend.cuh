@@ -14,6 +14,11 @@ constexpr int kMaxCtas = 2 * kSms;
 // leave m as it is, and a p as small as 2^-126 still counts in the sum of a
 // row whose values' scales differ by 2^120.
 constexpr float kMaxP = 15.75f, kRaiseP = 6.f;
+// Sums of exponentials are kept as l = sum p kSumUnit / b over the value scales
+// b.  The cache stores rows of 2^-100 to 2^128, b from 2^-109 to 2^121; with p up
+// to 2^16, 2^18 keys of the smallest scale stay below 2^127, and the unit over
+// a scale keeps its 24 bits up to b = 2^109 (12 at the largest).
+constexpr float kSumUnit = 0x1p-17f;
 constexpr int kFewRows = 32;            // query rows of an item of the kernel for few rows, at most
 
 // ---------------------------------------------------------------------------
@@ -212,6 +217,27 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// What makes an item's sums its outputs, sums * inv * post: the power of two
+// apart keeps inv a normal number.  A row without keys (l = 0) gets zeros.
+struct Norm {
+    float inv, post;
+};
+__device__ __forceinline__ Norm norm_of(float l) {
+    const bool large = l > 1.f;
+    return Norm{l == 0.f ? 0.f : (large ? kSumUnit * 0x1p43f : kSumUnit) / l, large ? 0x1p-43f : 1.f};
+}
+
+// log(sum of exponentials) from the reference and the sum.  The sum's exponent
+// is taken apart, so that what cancels against m is a whole number.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    if (l == 0.f) return -INFINITY;
+    if (!(l < INFINITY)) return l;
+    const bool tiny = l < 0x1p-100f;
+    const uint32_t u = __float_as_uint(tiny ? l * 0x1p60f : l);
+    const int e = (int)(u >> 23) - 127 + (tiny ? 17 - 60 : 17);          // (17: kSumUnit)
+    return ((m + (float)e) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u))) * 0.6931471805599453f;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }

@@ -144,7 +144,7 @@ __device__ __forceinline__ void token_scales(const AttendParams& p, bool some, f
     const bool fine = vs > 0.f && vs < INFINITY;
     sc[0] = some ? ks * p.scale_log2 : 0.f;
     sc[TK] = !some ? -INFINITY : fine ? __log2f(vs) : __int_as_float(0x7fffffff);
-    sc[2 * TK] = some && fine ? __frcp_rn(vs) : 1.f;
+    sc[2 * TK] = some && fine ? __frcp_rn(vs) * kSumUnit : 1.f;
 }
 
 // The CTA's piece of the line, item by item.
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             float* part = p.part + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * part_floats(C::kRows, D);
             const int last = w.n_rows - 1 - q * 128 - 32 * quad;     // the warp's last row
             if (last >= 0) {
-                const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                const Norm norm = cut ? Norm{1.f, 1.f} : norm_of(l);
 #pragma unroll 1
                 for (int c = part_of * (D / 32 / SP); c < (part_of + 1) * (D / 32 / SP); ++c) {
                     uint32_t o[32];
@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                             uint32_t h[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                h[j] = bf16x2_of(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
+                                h[j] = bf16x2_of(__uint_as_float(o[8 * i + 2 * j]) * norm.inv * norm.post,
+                                                 __uint_as_float(o[8 * i + 2 * j + 1]) * norm.inv * norm.post);
                             *place(lane, 4 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         part[(size_t)C::kRows * D + r] = m;
                         part[(size_t)C::kRows * (D + 1) + r] = l;
                     } else if (p.lse) {
-                        p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                        p.lse[orow] = lse_of(m, l);
                     }
                 }
             }

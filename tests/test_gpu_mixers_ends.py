@@ -47,3 +47,41 @@ def attended(cache, Hq, Hk, D, q, ns, scale=None, **kw):
 def test_a_window_wider_than_any_cache(window, Hq, Hk, D, ns, kv):
     """Fewer places than new tokens and a window that means "no limit": position - window must not wrap."""
     check_attend("int8", Hq, Hk, D, 16, ns, kv, window=window, seed=D)
+
+
+# ----------------------------------------------------------------------------
+# the size of value rows
+# ----------------------------------------------------------------------------
+# new tokens and query heads per key head: 5 rows, 80 (converted on the way), 600 and 1200 (images)
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,group", [(1, 4), (20, 4), (150, 4)])
+@pytest.mark.parametrize("log2", [-100, -60, 90])
+def test_value_rows_of_any_size(fmt, n, group, log2):
+    """Long contexts of equal scores whose value rows are all very small or large: the sum of exponentials over the
+    scales has to stay inside fp32."""
+    m, D = 16384, 64
+    g = torch.Generator().manual_seed(n)
+    cache = R.Cache(fmt, 1, D, 1024, [m])
+    v = (2 * torch.rand(m, 1, D, generator=g) - 1) * 2.0 ** log2
+    v[:, :, 0] = 2.0 ** log2                     # (every row's largest: none is stored as zeros)
+    cache.put("v", 0, range(m), v.bfloat16())
+    attended(cache, group, 1, D, torch.zeros(n, group, D).bfloat16(), [n], causal=False)
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (20, 4), (70, 4)])
+def test_rising_scores_over_small_value_rows(n, group):
+    """Scores that rise just too little to move the reference, over rows of 2^-100, in pieces of several key tiles."""
+    m, D, Hk = 8192, 64, 4
+    g = torch.Generator().manual_seed(n)
+    cache = R.Cache("e4m3", Hk, D, 1024, [m] * 4)
+    v = (2 * torch.rand(m, Hk, D, generator=g) - 1) * 2.0 ** -100
+    v[:, :, 0] = 2.0 ** -100
+    k = torch.zeros(m, Hk, D)
+    k[:, :, 0] = torch.where(torch.arange(m) % 512 < 128, 0.0, 6.0)[:, None]
+    for s in range(4):
+        cache.put("v", s, range(m), v.bfloat16())
+        cache.put("k", s, range(m), k.bfloat16())
+    q = torch.zeros(4 * n, Hk * group, D)
+    q[:, :, 0] = 1
+    attended(cache, Hk * group, Hk, D, q.bfloat16(), [n] * 4, scale=1.0, causal=False)
