@@ -402,8 +402,11 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  *        (-inf for a row without keys), for joining parts of a context
  * Products are of the bf16 queries and the stored codes as fp16, exact, with
  * fp32 sums; the probabilities (times the value's scale) are rounded to
- * fp16.  The scales of the value rows that one query sees may lie up to
- * 2^100 apart; those from 2^-109 (the smallest that lmoe_kv_append stores) to
+ * fp16.  A value row of zeros (scale 0, or codes of zeros under the scale 1
+ * that lmoe_kv_append stores) counts in the sum of exponentials and nowhere
+ * else; a value scale that is no number from 0 on makes the queries that see
+ * its row NaN.  The scales of the other value rows that one query sees may lie
+ * up to 2^100 apart; those from 2^-109 (the smallest that lmoe_kv_append stores) to
  * 2^109 leave 24 bits in the sum of exponentials, larger ones 12 or more.
  * Results do not depend on timing.
  * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that

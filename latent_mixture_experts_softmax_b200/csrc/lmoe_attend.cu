@@ -7,7 +7,8 @@
 // (values),
 //   t_j = scale log2(e) a_j (q . ck_j) + log2(b_j),   p_j = 2^(t_j - m),
 //   out = sum_j p_j cv_j / sum_j p_j (1 / b_j)
-// (the second sum in a unit that keeps it inside fp32, kSumUnit).
+// (the second sum in a unit that keeps it inside fp32, kSumUnit; rows of zeros
+// enter it by their bare score, kZeroDrop).
 // Folding the value's scale into the exponent keeps the second product in
 // fp16 whatever the scales are: p is below 2^16 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
@@ -43,6 +44,7 @@ using namespace attend;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = kFewRows;
+constexpr float kNull = 0x1p127f;       // stands for the inverse of a scale of 0
 
 // ---------------------------------------------------------------------------
 // arithmetic
@@ -99,6 +101,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
     __shared__ float s_qscale[kMaxRows];
     __shared__ int s_pos[kMaxRows];
     __shared__ float s_m[kWarps][kMaxRows], s_l[kWarps][kMaxRows];
+    __shared__ uint32_t s_any[NS == 2 ? kWarps : 1][4];
 
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -294,12 +297,18 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                 odd ^= 1;
             }
             const float k0 = ks[0], k1 = ks[1];
-            // scales that are no positive numbers make a score NaN (a row
-            // stored as NaN) or belong to places that are masked below
-            const bool f0 = vs[0] > 0.f && vs[0] < INFINITY, f1 = vs[1] > 0.f && vs[1] < INFINITY;
-            const float lv0 = f0 ? __log2f(vs[0]) : __int_as_float(0x7fffffff);
-            const float lv1 = f1 ? __log2f(vs[1]) : __int_as_float(0x7fffffff);
-            const float iv0 = f0 ? __frcp_rn(vs[0]) * kSumUnit : 1.f, iv1 = f1 ? __frcp_rn(vs[1]) * kSumUnit : 1.f;
+            // scales that are no numbers from 0 on make a score NaN (a row stored
+            // as NaN) or belong to places that are masked below; 0 and 1 may be
+            // rows of zeros (looking for them in this order costs a batch of 64
+            // single tokens nothing; as part of the branches for masks or for m: 4%)
+            const bool zeros = __any_sync(0xffffffffu, vs[0] == 0.f || vs[0] == 1.f || vs[1] == 0.f || vs[1] == 1.f);
+            float lv0 = vs[0] < INFINITY ? __log2f(vs[0]) : __int_as_float(0x7fffffff);
+            float lv1 = vs[1] < INFINITY ? __log2f(vs[1]) : __int_as_float(0x7fffffff);
+            const float iv0 = fminf(fabsf(__frcp_rn(vs[0]) * kSumUnit), kNull), iv1 = fminf(fabsf(__frcp_rn(vs[1]) * kSumUnit), kNull);
+            if (__builtin_expect(zeros, 0)) {            // the bare score
+                lv0 = vs[0] == 0.f ? 0.f : lv0;
+                lv1 = vs[1] == 0.f ? 0.f : lv1;
+            }
             const int tok = st << 4;
             const bool whole = ok && tok + 15 <= min(pos_lo, it.rows.kv - 1) && tok > win_lo;
             const bool ok_now = ok;
@@ -334,6 +343,32 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
 #pragma unroll
                         for (int i = 0; i < C::kVw; ++i) vw[h][i] = 0u;
             }
+            bool z0 = false, z1 = false;                 // rows g and g + 8 are zeros
+            if (__builtin_expect(zeros, 0)) {
+                // bit g * 4 + t of any[h] tells of codes in row 2 t + (h & 1) + 8 (h >> 1)
+                uint32_t any[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w = 0;
+#pragma unroll
+                    for (int i = 0; i < C::kVw; ++i) w |= vw[h][i];
+                    any[h] = __ballot_sync(0xffffffffu, (FMT == LMOE_KV_INT8 ? w : w & 0x7f7f7f7fu) != 0);
+                }
+                if (NS == 2) {       // (the other warp's columns; the next step's barrier keeps it from writing anew too early)
+                    if (lane < 4) s_any[warp][lane] = lane == 0 ? any[0] : lane == 1 ? any[1] : lane == 2 ? any[2] : any[3];
+                    named_bar_sync(1 + grp, 64);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) any[h] |= s_any[warp ^ 1][h];
+                }
+                const uint32_t row_g = 0x11111111u << (g >> 1);
+                z0 = iv0 == kNull || (iv0 == kSumUnit && !((g & 1 ? any[1] : any[0]) & row_g));
+                z1 = iv1 == kNull || (iv1 == kSumUnit && !((g & 1 ? any[3] : any[2]) & row_g));
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < 2 ? z0 : z1) s[r][i] -= kZeroDrop;
+            }
             // m is raised rarely, so most steps skip the exchange between
             // lanes and the rescaling
 #pragma unroll
@@ -353,15 +388,26 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 8));
                         n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 16));
                         n = fmaxf(n - kRaiseP, m[r][i]);
-                        const float f = m[r][i] == n ? 1.f : ex2(m[r][i] - n);
+                        const float h = m[r][i] == n ? 1.f : ex2(0.5f * (m[r][i] - n)), f = h * h;
                         m[r][i] = n;
-                        l[r][i] *= f;
+                        l[r][i] = twice(l[r][i], h);
 #pragma unroll
                         for (int j = 0; j < C::kTiles; ++j) {
                             o[j][r][i] *= f;
                             o[j][r][i + 2] *= f;
                         }
                     }
+            }
+            if (__builtin_expect(zeros, 0)) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < 2 ? z0 : z1) {
+                            const float mm = m[r][i & 1] == -INFINITY ? 0.f : m[r][i & 1];
+                            l[r][i & 1] += ex2(s[r][i] + kZeroDrop - mm) * kSumUnit;
+                            s[r][i] = -INFINITY;
+                        }
             }
             uint32_t pb[NR][2];
 #pragma unroll
@@ -420,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
                 const float nn = n == -INFINITY ? 0.f : n;
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < C::kGroups; ++w) sum += s_l[w][rr] * ex2(s_m[w][rr] - nn);
+                for (int w = 0; w < C::kGroups; ++w) sum += twice(s_l[w][rr], ex2(0.5f * (s_m[w][rr] - nn)));
                 mtot[r][i] = n;
                 ltot[r][i] = sum;
                 const float f = ex2(m[r][i] - nn);
@@ -562,10 +608,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, in
         float f[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            const float x = ex2(q[rr[i]] - (m[i] == -INFINITY ? 0.f : m[i]));
-            f[i] = k0 + lane < np ? x : 0.f;
-            const float y = q[rows + rr[i]];
-            l[i] = k0 + lane < np ? fmaf(f[i], y, l[i]) : l[i];
+            const float h = ex2(0.5f * (q[rr[i]] - (m[i] == -INFINITY ? 0.f : m[i])));
+            f[i] = k0 + lane < np ? h * h : 0.f;
+            const float y = twice(q[rows + rr[i]], h);
+            l[i] = k0 + lane < np ? l[i] + y : l[i];
         }
         const int n = min(32, np - k0);
         int j = FEW ? warp : 0;

@@ -19,6 +19,14 @@ constexpr float kMaxP = 15.75f, kRaiseP = 6.f;
 // to 2^16, 2^18 keys of the smallest scale stay below 2^127, and the unit over
 // a scale keeps its 24 bits up to b = 2^109 (12 at the largest).
 constexpr float kSumUnit = 0x1p-17f;
+// Value rows of zeros (scale 0, or codes of zeros under the scale 1 that the
+// cache stores with them) have no size, so their scale says nothing about the
+// reference: left in t, one of them among rows of 1e-8 pushed the others'
+// probabilities out of fp16.  They stay out of the products, and enter the sum
+// as 2^(s - m) with the bare score s in fp32, which has room for s far above m
+// (2^18 keys at kMaxP + kZeroDrop, in kSumUnit: 2^123).  Towards m they count as
+// t = s - kZeroDrop.
+constexpr float kZeroDrop = 106.f;
 constexpr int kFewRows = 32;            // query rows of an item of the kernel for few rows, at most
 
 // ---------------------------------------------------------------------------
@@ -219,6 +227,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// x h^2 with h = 2^(d / 2), for d down to twice the exponents' range: a sum of
+// rows of zeros can stand that far above its reference.
+__device__ __forceinline__ float twice(float x, float h) { return x * h * h; }
+
 // What makes an item's sums its outputs, sums * inv * post: the power of two
 // apart keeps inv a normal number.  A row without keys (l = 0) gets zeros.
 struct Norm {
@@ -270,9 +282,9 @@ __device__ __forceinline__ uint32_t biased(uint32_t w) { return FMT == LMOE_KV_I
 __host__ __device__ constexpr int many_rows(int D) { return D == 256 ? 128 : 256; }
 
 // Images of key tiles: tokens of a tile, bytes (keys and values in fp16, three
-// floats a token), and what a workspace holds of them: half of L2.
+// floats and a bit a token), and what a workspace holds of them: half of L2.
 __host__ __device__ constexpr int image_tokens(int) { return 64; }
-__host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12); }
+__host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12) + 16; }
 constexpr size_t kImageBytes = 64u << 20;
 // Images are made for more row tiles than kImageRowTiles, and for two to four
 // where the contexts are brief and one group takes all (300 rows over 8000

@@ -62,7 +62,9 @@ struct Many {
     static constexpr int kThreads = (kMmaWarp + NQ) * 32;
     static constexpr size_t kQBytes = 128 * D * 2;    // one query tile
     static constexpr size_t kOpBytes = TK * D * 2;    // one stage of keys or values
-    static constexpr size_t kScaleBytes = 3 * TK * 4; // per token: key scale, log2 and inverse of the value scale
+    // per token: key scale, log2 and inverse of the value scale; then a bit per
+    // token whose value row is all zeros
+    static constexpr size_t kScaleBytes = 3 * TK * 4 + 16;
     static constexpr size_t kImage = 2 * kOpBytes + kScaleBytes;   // keys, values, scales of a tile
     static constexpr size_t kSmem = 1024 + NQ * kQBytes + 2 * NST * kOpBytes + 4 * kScaleBytes + 512;
     static constexpr uint32_t kColO = 256;            // tensor memory: scores from 0 ((NB q + b) * TK), sums from 256 (q * D)
@@ -138,13 +140,33 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
     return r;
 }
 
-// What the softmax needs of a token.  A place without one weighs nothing; a
-// value scale that is no positive number makes its token's scores NaN.
-__device__ __forceinline__ void token_scales(const AttendParams& p, bool some, float ks, float vs, float* sc, int TK) {
+// Whether a value row's codes are all zeros (nearly every other row shows in
+// its first 16 bytes).
+template <int D, int FMT>
+__device__ __forceinline__ bool zero_codes(const uint8_t* row) {
+#pragma unroll 1
+    for (int i = 0; i < D / 16; ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(row) + i);
+        const uint32_t w = u.x | u.y | u.z | u.w;
+        if (FMT == LMOE_KV_INT8 ? w : w & 0x7f7f7f7fu) return false;
+    }
+    return true;
+}
+
+// What the softmax needs of token `tok` of a tile, whose place is `row` (a warp
+// has 32 tokens).  A place without one weighs nothing, nor does a value row of
+// zeros but in the sum; a value scale that is no number from 0 on makes its
+// token's scores NaN.
+template <int D, int FMT>
+__device__ __forceinline__ void token_scales(const AttendParams& p, bool some, size_t row, float ks, float vs, float* sc, int tok) {
+    constexpr int TK = image_tokens(D);
     const bool fine = vs > 0.f && vs < INFINITY;
-    sc[0] = some ? ks * p.scale_log2 : 0.f;
-    sc[TK] = !some ? -INFINITY : fine ? __log2f(vs) : __int_as_float(0x7fffffff);
-    sc[2 * TK] = some && fine ? __frcp_rn(vs) * kSumUnit : 1.f;
+    const bool zero = some && (vs == 0.f || (vs == 1.f && zero_codes<D, FMT>(p.v + row * D)));
+    sc[tok] = some ? ks * p.scale_log2 : 0.f;
+    sc[TK + tok] = !some || zero ? -INFINITY : fine ? __log2f(vs) : __int_as_float(0x7fffffff);
+    sc[2 * TK + tok] = some && fine ? __frcp_rn(vs) * kSumUnit : 1.f;
+    const uint32_t bits = __ballot_sync(0xffffffffu, zero);
+    if ((tok & 31) == 0) reinterpret_cast<uint32_t*>(sc + 3 * TK)[tok >> 5] = bits;
 }
 
 // The CTA's piece of the line, item by item.
@@ -352,13 +374,15 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                 for (int t = w.t0; t < w.t1; ++t, ++n, ++cnt) {
                     if (CH && (int)(n & 1) != half) continue;
                     const int st = n & 3, b = NB * q + (cnt & (NB - 1));
-                    dead = !wait(&sc_full[st], n >> 2) || !wait(&s_full[b], cnt >> kBufLog2);
+                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
+                    dead = !wait(&sc_full[st], n >> 2);
+                    const uint2 zeros = *reinterpret_cast<const uint2*>(ks + 3 * TK / 4);
+                    dead = dead || !wait(&s_full[b], cnt >> kBufLog2);
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     tc_fence_after();
                     __syncwarp();
                     const uint32_t tS = tmem + lanes + b * TK;
-                    const float4* ks = reinterpret_cast<const float4*>(ssc + st * (C::kScaleBytes / 4));
                     const int tok0 = t * TK;
                     // keys this row sees: columns lo .. hi - 1
                     const int hi = p.causal ? pos + 1 - tok0 : TK;
@@ -400,6 +424,27 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         top = fmaxf(top, a);
                     }
                     float was = m;                       // the reference of the tile before
+                    if (__builtin_expect(zeros.x | zeros.y, 0)) {
+                        // tokens whose value row is all zeros (their exponents are -infinity)
+                        auto each = [&](auto f) {
+#pragma unroll 1
+                            for (unsigned long long z = (unsigned long long)zeros.y << 32 | zeros.x; z; z &= z - 1) {
+                                const int c = __ffsll(z) - 1;
+                                __syncwarp();
+                                const float y = tmem_ld_32x32b_x1(tS + c);
+                                f(c < lo || c >= hi ? -INFINITY : y * reinterpret_cast<const float*>(ks)[c] * scale);
+                            }
+                        };
+                        float ztop = -INFINITY;
+                        each([&](float y) { ztop = fmaxf(ztop, y - kZeroDrop); });
+                        if (ztop > m + kMaxP) {          // as below for all of the tile
+                            const float n = ceilf(ztop) - kRaiseP;
+                            l = twice(l, ex2(0.5f * (m - n)));
+                            m = n;
+                        }
+                        each([&](float y) { l += ex2(y - (m == -INFINITY ? 0.f : m)) * kSumUnit; });
+                        top = fmaxf(top, ztop);
+                    }
                     if (CH) {
                         was = -INFINITY;
                         if (t > w.t0) {
@@ -418,7 +463,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         if (lane == 0) mbar_arrive(&chain[quad]);
                     }
                     if (__any_sync(0xffffffffu, m != now)) {     // (CH: also where the other warp has raised it)
-                        l *= m == now ? 1.f : ex2(m - now);
+                        l = m == now ? l : twice(l, ex2(0.5f * (m - now)));
                         m = now;
                     }
                     if (grow && t > w.t0) {              // the sums of the earlier tiles are in tensor memory
@@ -478,7 +523,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                     dead = __any_sync(0xffffffffu, dead);
                     if (dead) break;
                     const float now = s_m[(n - 1) & 1][row];
-                    s_l[half][row] = l *= m == now ? 1.f : ex2(m - now);
+                    s_l[half][row] = l = m == now ? l : twice(l, ex2(0.5f * (m - now)));
                     m = now;
                     dead = !meet();
                     if (dead) break;
@@ -519,9 +564,11 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
                         for (int i = 0; i < 4; ++i) {            // through the query tile's place, for whole-row stores
                             uint32_t h[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                h[j] = bf16x2_of(__uint_as_float(o[8 * i + 2 * j]) * norm.inv * norm.post,
-                                                 __uint_as_float(o[8 * i + 2 * j + 1]) * norm.inv * norm.post);
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 y = unpack2(mul2(mul2(pack2(__uint_as_float(o[8 * i + 2 * j]), __uint_as_float(o[8 * i + 2 * j + 1])),
+                                                                   pack2(norm.inv, norm.inv)), pack2(norm.post, norm.post)));
+                                h[j] = bf16x2_of(y.x, y.y);
+                            }
                             *place(lane, 4 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }
@@ -615,6 +662,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
         struct Raw {
             uint4 v[PASSES];
             float ksc, vsc;
+            uint32_t row;                        // this thread's token, in the scale arrays (caches of 2^32 rows fit no card)
             uint32_t none;                       // bit i: row i of this thread holds no token, bit 31: its scales
         };
         uint32_t pid = ~0u;                      // lane i: page of tokens 16 i .. of the next tile
@@ -657,8 +705,9 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             const long long first = __shfl_sync(0xffffffffu, at, (tid & (TK - 1)) >> 4);
             const bool good = keys && first >= 0 && tid < there;
             raw.none |= good ? 0u : 1u << 31;
-            raw.ksc = __ldg(p.ks + (good ? first + (tid & 15) : 0ll));
-            raw.vsc = __ldg(p.vs + (good ? first + (tid & 15) : 0ll));
+            raw.row = good ? (uint32_t)first + (tid & 15) : 0;
+            raw.ksc = __ldg(p.ks + raw.row);
+            raw.vsc = __ldg(p.vs + raw.row);
         };
         Raw cur;
         settle();
@@ -681,7 +730,7 @@ __global__ void __launch_bounds__(Many<D, IMG>::kThreads, 1) k_attend_many(Atten
             dead = __any_sync(0xffffffffu, dead);
             if (dead) break;
             if (keys && tid < TK)
-                token_scales(p, !(cur.none >> 31), cur.ksc, cur.vsc, ssc + (n & 3) * (C::kScaleBytes / 4) + tid, TK);
+                token_scales<D, FMT>(p, !(cur.none >> 31), cur.row, cur.ksc, cur.vsc, ssc + (n & 3) * (C::kScaleBytes / 4), tid);
             if (cur.none << 1) {                 // codes behind the last token may be anything, a NaN code too
 #pragma unroll
                 for (int i = 0; i < PASSES; ++i)
@@ -841,8 +890,8 @@ __global__ void __launch_bounds__(256) k_attend_images(AttendParams p) {
     }
     if (threadIdx.x < TK) {
         const long long at = place(tok0 + threadIdx.x);
-        token_scales(p, at >= 0, at >= 0 ? __ldg(p.ks + at) : 0.f, at >= 0 ? __ldg(p.vs + at) : 0.f,
-                     reinterpret_cast<float*>(img + 2 * C::kOpBytes) + threadIdx.x, TK);
+        token_scales<D, FMT>(p, at >= 0, (size_t)at, at >= 0 ? __ldg(p.ks + at) : 0.f, at >= 0 ? __ldg(p.vs + at) : 0.f,
+                             reinterpret_cast<float*>(img + 2 * C::kOpBytes), threadIdx.x);
     }
 }
 

@@ -54,6 +54,50 @@ def test_a_window_wider_than_any_cache(window, Hq, Hk, D, ns, kv):
 # ----------------------------------------------------------------------------
 # new tokens and query heads per key head: 5 rows, 80 (converted on the way), 600 and 1200 (images)
 
+ROWS = [(5, 1), (40, 2), (150, 4), (300, 4)]
+
+
+@pytest.mark.parametrize("fmt,D", [("int8", 128), ("e4m3", 256), ("int8", 64)])
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("size", [1e-8, 1.0, 1e20])
+@pytest.mark.parametrize("zero_scale", [1.0, 0.0])
+def test_value_rows_of_zeros(fmt, D, n, group, size, zero_scale):
+    """A row of zeros adds to the sum of exponentials and to nothing else, whatever its scale says (1 as the cache
+    stores it, 0 as other encoders do) and however much larger its score or smaller the other rows' values are: whole
+    tiles of them, single ones, one whole sequence."""
+    m = n + 100
+    g = torch.Generator().manual_seed(n)
+    cache = R.Cache(fmt, 1, D, 16, [m, m], seed=3)
+    v = (torch.randn(m, 1, D, generator=g) * size).bfloat16()
+    k = torch.randn(m, 1, D, generator=g)
+    zero = torch.rand(m, generator=g) < 0.1
+    zero[:70] = True
+    zero[m - n // 2] = True
+    v[zero] = 0
+    k[zero] *= 3
+    for s in range(2):
+        cache.put("k", s, range(m), k.bfloat16())
+        cache.put("v", s, range(m), v if s == 0 else torch.zeros_like(v))
+    if zero_scale != 1.0:
+        for s in range(2):
+            for pos in range(m):
+                if zero[pos] or s == 1:
+                    cache.scale["v"][cache.table[s, pos // 16].item(), :, pos % 16] = zero_scale
+    q = torch.randn(2 * n, group, D, generator=g).bfloat16()
+    out = attended(cache, group, 1, D, q, [n, n])
+    assert (out[n:] == 0).all()
+
+
+@pytest.mark.parametrize("n,group", [(5, 1), (40, 2), (300, 4)])
+def test_a_scale_of_zero_makes_its_codes_zeros(n, group):
+    """value = code * scale, codes that are not zero under a scale of 0 included."""
+    cache = R.Cache("int8", 1, 64, 16, [n + 90])
+    g = torch.Generator().manual_seed(1)
+    for pos in torch.randperm(n + 90, generator=g)[:30].tolist():
+        cache.scale["v"][cache.table[0, pos // 16].item(), :, pos % 16] = 0.0
+    attended(cache, group, 1, 64, torch.randn(n, group, 64, generator=g).bfloat16(), [n])
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("n,group", [(1, 4), (20, 4), (150, 4)])
 @pytest.mark.parametrize("log2", [-100, -60, 90])
@@ -85,3 +129,17 @@ def test_rising_scores_over_small_value_rows(n, group):
     q = torch.zeros(4 * n, Hk * group, D)
     q[:, :, 0] = 1
     attended(cache, Hk * group, Hk, D, q.bfloat16(), [n] * 4, scale=1.0, causal=False)
+
+
+@pytest.mark.parametrize("n,group", ROWS)
+def test_zeros_before_rows_of_other_sizes(n, group):
+    """Rows of zeros come first, then rows of 2^-99, of 2^-20 and of 2^40 that only later queries see."""
+    m, D = n + 200, 64
+    g = torch.Generator().manual_seed(n)
+    for sizes in ([0, 2.0 ** -98], [0, 2.0 ** -98, 2.0 ** -20], [0, 2.0 ** 40], [2.0 ** 40, 0]):
+        cache = R.Cache("int8", 1, D, 16, [m])
+        v = torch.randn(m, 1, D, generator=g)
+        for i, x in enumerate(sizes):
+            v[m * i // len(sizes):m * (i + 1) // len(sizes)] *= x
+        cache.put("v", 0, range(m), v.bfloat16())
+        attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
