@@ -423,7 +423,10 @@ LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, c
  * Batches with max_new up to 16 run in one launch, longer sequences in chunks
  * of 32 tokens.  The state and every sum are fp32; fp32 operands that go into
  * the state enter the products with all their bits, those that only go into
- * out with 16.  Results do not depend on timing. */
+ * out with 16.  A number that is not finite leaves earlier tokens, other heads
+ * and, in v, other columns as they are; it makes outputs from its token on and
+ * the state NaN or infinite (in q: its token's outputs only).  Results do not
+ * depend on timing. */
 typedef struct {
     int n_heads;       /* heads of v, the gates and the state: a multiple of n_qk_heads */
     int n_qk_heads;    /* heads of q and k; head j uses q, k head j / (n_heads / n_qk_heads) */

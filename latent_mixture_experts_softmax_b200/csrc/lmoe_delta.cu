@@ -21,6 +21,12 @@
 // with S^T as the first operand a result's registers are the next product's
 // operand as they are.
 //
+// A number that is not finite must not reach the tokens before it: the zeros
+// above T's and P's diagonals are factors of the products like any other.  So
+// where an update U is not finite, k_delta_scan cuts the right-hand sides and
+// updates off at the first token that is not, a column at a time, and makes
+// what follows it NaN; k_delta_short falls back on the recurrence.
+//
 // k_delta_short takes a few tokens (one chunk of up to 16) in one launch,
 // bound by the state's bytes, read and written once.  (The plain recurrence,
 // two dot products and a rank-one update a token in fp32, spends 16
@@ -151,6 +157,43 @@ __device__ __forceinline__ void mul3(float (&acc)[4], const uint32_t (&a)[3][4],
     mma_bf16(acc, a[0], b.z, b.w);
     mma_bf16(acc, a[0], b.x, b.y);
 }
+// A lane's results of J tiles of 8 tokens: tokens 8 j + 2 t + (i & 1) of the
+// columns i >> 1.
+template <int J>
+__device__ __forceinline__ bool not_finite(const float (&x)[J][4]) {
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = fmaf(x[j][i], 0.f, z[i]);
+    return (z[0] + z[1]) + (z[2] + z[3]) != 0.f;
+}
+// The first token of each column that is not finite (or rounds to a bf16 that
+// is not), where it comes before at[].
+template <int J>
+__device__ __forceinline__ int2 first_bad(const float (&x)[J][4], int t, int2 at) {
+    int f[2] = {at.x, at.y};
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!(fabsf(x[j][i]) < 0x1.ffp127f)) f[i >> 1] = min(f[i >> 1], 8 * j + 2 * t + (i & 1));
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) f[c] = min(f[c], __shfl_xor_sync(0xffffffffu, f[c], o));
+    return make_int2(f[0], f[1]);
+}
+// `with` from token at[] on.
+template <int J>
+__device__ __forceinline__ void cut_off(float (&x)[J][4], int t, int2 at, float with) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * j + 2 * t + (i & 1) >= (i < 2 ? at.x : at.y)) x[j][i] = with;
+}
+
 // An 8 x 8 matrix of 16-bit numbers, two a lane, transposed: pairs of tokens
 // of a column become pairs of columns of a token.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -294,6 +337,13 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
             xl[lane] = gl;
             __syncwarp();
             if (!(warp & 1)) {
+                // the first token with a number that is not finite: its row of A T11
+                // below would meet the zeros of earlier rows of T22
+                bool bad = !(fabsf(b) < INFINITY) || !(gt < INFINITY);
+                if (!(kk[lane][lane] < INFINITY))
+                    for (int i = 0; i < DK; ++i) bad |= (sk[lane][i] & 0x7fffu) >= 0x7f80u;
+                const unsigned bads = __ballot_sync(0xffffffffu, bad);
+                const int first = bads ? __ffs(bads) - 1 : kC;
                 float(*m)[kC + 4] = sa[warp >> 1];
                 const float br = b * rk;
 #pragma unroll 8
@@ -341,7 +391,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) k_delta_chunks(DeltaParams p,
                             y[2] = fmaf(a.z, x[j + 2], y[2]);
                             y[3] = fmaf(a.w, x[j + 3], y[3]);
                         }
-                        m[rb + i][16 + cj] = (y[0] + y[1]) + (y[2] + y[3]);
+                        m[rb + i][16 + cj] = 16 + rb + i < first ? (y[0] + y[1]) + (y[2] + y[3]) : 0.f;
                     }
                     __syncwarp();
 #pragma unroll
@@ -634,47 +684,89 @@ __global__ void __launch_bounds__(kShortThreads, 4) k_delta_short(DeltaParams p)
             const uint2 l = s_tl[j][lane];
             mul3(u[j], a, f, l);
         }
-        // ---- out^T
-        split_a(u[0], u[1], hi, lo);
+        if (__builtin_expect(__any_sync(0xffffffffu, not_finite(u)), 0)) {
+            // numbers that are not finite: the recurrence itself, a token after the other
+            const size_t col = (size_t)h * p.DV + cb * kShortN + warp * 16 + g + 8 * t;
+            for (int i = 0; i < r.n; ++i) {
+                const float decay = exp_of(i ? (s_gh[0][i] - s_gh[0][i - 1]) + (s_gl[0][i] - s_gl[0][i - 1]) : s_gh[0][0] + s_gl[0][0]);
+                const float rk = s_rk[i], b = s_b[i];
+                float y[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint4 f = s_p[j][lane];
-            mma_bf16(o[j], hi, f.x, f.y);
-            mma_bf16(o[j], hi, f.z, f.w);
-            mma_bf16(o[j], lo, f.x, f.y);
-        }
+                for (int j = 0; j < NT; ++j) {
+                    const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sk[i][8 * j + 2 * t]));
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+                    for (int e = 0; e < 4; ++e) {
+                        S[j][e] *= decay;
+                        y[e >> 1] = fmaf(e & 1 ? f.y : f.x, S[j][e], y[e >> 1]);
+                    }
+                }
+                float z[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t y = transposed(pack_bf16(o[j][2 * i], o[j][2 * i + 1]));
-                const int row = 8 * j + g;
-                if (row < r.n)
-                    *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kShortN + warp * 16 + 8 * i +
-                                                 2 * t) = y;
+                for (int c = 0; c < 2; ++c) {
+                    y[c] += __shfl_xor_sync(0xffffffffu, y[c], 1);
+                    y[c] += __shfl_xor_sync(0xffffffffu, y[c], 2);
+                    y[c] = b * rk * (bf16_bits_to_f32(sv[i][warp * 16 + g + 8 * c]) - rk * y[c]);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sk[i][8 * j + 2 * t]));
+                    const float2 q = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(&sq[i][8 * j + 2 * t]));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[j][e] = fmaf(e & 1 ? f.y : f.x, y[e >> 1], S[j][e]);
+                        z[e >> 1] = fmaf(e & 1 ? q.y : q.x, S[j][e], z[e >> 1]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    z[c] += __shfl_xor_sync(0xffffffffu, z[c], 1);
+                    z[c] += __shfl_xor_sync(0xffffffffu, z[c], 2);
+                }
+                if (t < 2) p.out[(size_t)(r.q0 + i) * p.H * p.DV + col] = f32_to_bf16_bits((t ? z[1] : z[0]) * s_rq[i]);
             }
-        // ---- the state
+        } else {
+            // ---- out^T
+            split_a(u[0], u[1], hi, lo);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 f = *reinterpret_cast<const float2*>(&s_wf[8 * j + 2 * t]);
-            u[j][0] *= f.x;
-            u[j][1] *= f.y;
-            u[j][2] *= f.x;
-            u[j][3] *= f.y;
-        }
-        split_a(u[0], u[1], a);
-        const float last = s_last;
+            for (int j = 0; j < 2; ++j) {
+                const uint4 f = s_p[j][lane];
+                mma_bf16(o[j], hi, f.x, f.y);
+                mma_bf16(o[j], hi, f.z, f.w);
+                mma_bf16(o[j], lo, f.x, f.y);
+            }
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-            uint32_t bk[4];
-            ldm4t(bk, &sk[lane & 15][16 * j + (lane >> 4) * 8]);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t y = transposed(pack_bf16(o[j][2 * i], o[j][2 * i + 1]));
+                    const int row = 8 * j + g;
+                    if (row < r.n)
+                        *reinterpret_cast<uint32_t*>(p.out + ((size_t)(r.q0 + row) * p.H + h) * p.DV + cb * kShortN + warp * 16 + 8 * i +
+                                                     2 * t) = y;
+                }
+            // ---- the state
 #pragma unroll
-                for (int o = 2; o >= 0; --o) mma_bf16(d, a[o], bk[2 * i], bk[2 * i + 1]);
+            for (int j = 0; j < 2; ++j) {
+                const float2 f = *reinterpret_cast<const float2*>(&s_wf[8 * j + 2 * t]);
+                u[j][0] *= f.x;
+                u[j][1] *= f.y;
+                u[j][2] *= f.x;
+                u[j][3] *= f.y;
+            }
+            split_a(u[0], u[1], a);
+            const float last = s_last;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[2 * j + i][e] = fmaf(S[2 * j + i][e], last, d[e]);
+            for (int j = 0; j < NT / 2; ++j) {
+                uint32_t bk[4];
+                ldm4t(bk, &sk[lane & 15][16 * j + (lane >> 4) * 8]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int o = 2; o >= 0; --o) mma_bf16(d, a[o], bk[2 * i], bk[2 * i + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[2 * j + i][e] = fmaf(S[2 * j + i][e], last, d[e]);
+                }
             }
         }
     }
@@ -873,34 +965,47 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
         }
         // ---- U^T
         float u[4][4];
+        int2 cut = make_int2(kC, kC);            // the columns' first tokens that are not finite
+#pragma unroll 1
+        for (bool again = false;; again = true) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
+                for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t a[3][4];
-            split_a(ks[2 * k], ks[2 * k + 1], a);
-            const uint4* f = ft + 2 * k;
-            uint2 l[4];
+            for (int k = 0; k < 2; ++k) {
+                uint32_t a[3][4];
+                split_a(ks[2 * k], ks[2 * k + 1], a);
+                const uint4* f = ft + 2 * k;
+                uint2 l[4];
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) l[j] = x.d.tl[k ? j + 2 : j][lane];
-            // (mul3, of up to four tiles side by side)
+                for (int j = 2 * k; j < 4; ++j) l[j] = x.d.tl[k ? j + 2 : j][lane];
+                // (mul3, of up to four tiles side by side)
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[2], f[j].x, f[j].y);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[2], f[j].x, f[j].y);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].z, f[j].w);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].z, f[j].w);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], l[j].x, l[j].y);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], l[j].x, l[j].y);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].x, f[j].y);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].x, f[j].y);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].z, f[j].w);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].z, f[j].w);
 #pragma unroll
-            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].x, f[j].y);
+                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].x, f[j].y);
+            }
+            if (__builtin_expect(!__any_sync(0xffffffffu, not_finite(u)), 1)) break;
+            if (again) {                         // (rows of T from there on; sums that overflowed)
+                cut = first_bad(u, t, cut);
+                cut_off(u, t, cut, 0.f);
+                break;
+            }
+            cut = first_bad(ks, t, cut);
+            cut_off(ks, t, cut, 0.f);
         }
         // ---- the state
-        const float last = x.d.last[0];
+        const float last = x.d.last[0], last0 = cut.x < kC ? __int_as_float(0x7fffffff) : last,
+                    last1 = cut.y < kC ? __int_as_float(0x7fffffff) : last;
         uint32_t w[2][3][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -937,7 +1042,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[j0 + j][i] = fmaf(S[j0 + j][i], last, d[j][i]);
+                for (int i = 0; i < 4; ++i) S[j0 + j][i] = fmaf(S[j0 + j][i], i < 2 ? last0 : last1, d[j][i]);
         }
         // ---- out^T of 16 tokens
 #pragma unroll
@@ -957,6 +1062,8 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&sm.empty[st]);
+        if (__builtin_expect(__any_sync(0xffffffffu, min(cut.x, cut.y) < kC), 0))
+            cut_off(o, t, make_int2(cut.x - 16 * hf, cut.y - 16 * hf), __int_as_float(0x7fffffff));
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll

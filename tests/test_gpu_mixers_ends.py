@@ -143,3 +143,51 @@ def test_zeros_before_rows_of_other_sizes(n, group):
             v[m * i // len(sizes):m * (i + 1) // len(sizes)] *= x
         cache.put("v", 0, range(m), v.bfloat16())
         attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
+
+
+# ----------------------------------------------------------------------------
+# the gated delta rule and numbers that are not finite
+# ----------------------------------------------------------------------------
+
+def check_bad(n, H, Hq, DK, DV, spots, l2norm=True, seed=1):
+    """Tokens before a bad number, and heads and columns that it does not reach, are what they are without it."""
+    q, k, v, ld, beta = delta_inputs(n, H, Hq, DK, DV, seed, l2norm=l2norm)
+    for what, at, value in spots:
+        dict(q=q, k=k, v=v, decay=ld, beta=beta)[what][at] = value
+    S = torch.randn(1, H, DK, DV, generator=torch.Generator().manual_seed(seed + 1))
+    st = mixers.DeltaStates(H, Hq, DK, DV, l2norm=l2norm, state=S.to(DEV))
+    place = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = st.forward(*(x.to(DEV) for x in (q, k, v, ld, beta)), st.batch(R.starts([n]).to(DEV), place, place, n, n), st.workspace(n, 1, n))
+    o, S1 = R.delta(q, k, v, ld, beta, S[0], DK ** -0.5, l2norm)
+    fine = torch.isfinite(o)
+    assert torch.equal(torch.isfinite(out.cpu()), fine), "outputs that are finite"
+    assert torch.equal(torch.isfinite(st.state[0].cpu()), torch.isfinite(S1)), "states that are finite"
+    # bounds as for batches without bad numbers: a bf16 rounding, fp32's errors, operands of 16 bits
+    mag = S[0].abs().amax().double().clamp_min(1.0) * 4
+    tol = R.U_BF16 * 1.01 * o.abs() + 2.0 ** -14 * mag
+    got = torch.where(fine, out.double().cpu(), 0.0)
+    R.assert_within(got, torch.where(fine, o, 0.0), torch.where(fine, tol, 0.0), "out")
+    some = torch.isfinite(S1)
+    got = torch.where(some, st.state[0].double().cpu(), 0.0)
+    R.assert_within(got, torch.where(some, S1, 0.0), torch.full_like(S1, 32 * R.U_F32 * math.sqrt(DK + n) * mag.item()), "state")
+
+
+@pytest.mark.parametrize("H,Hq,DK,DV", [(2, 1, 64, 64), (4, 2, 128, 128), (3, 3, 64, 128), (2, 2, 128, 64)])
+@pytest.mark.parametrize("n,at", [(4, 2), (16, 9), (16, 15), (1, 0), (100, 40), (100, 53), (64, 31), (70, 69)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "decay", "beta"])
+def test_bad_numbers_reach_only_what_follows_them(H, Hq, DK, DV, n, at, what):
+    place = {"q": (at, Hq - 1, 5), "k": (at, Hq - 1, 7), "v": (at, H - 1, 33), "decay": (at, H - 1), "beta": (at, H - 1)}[what]
+    check_bad(n, H, Hq, DK, DV, [(what, place, math.nan)])
+
+
+@pytest.mark.parametrize("n,at", [(4, 2), (16, 9), (100, 40), (100, 60)])
+@pytest.mark.parametrize("what,value", [("v", math.inf), ("v", -math.inf), ("beta", math.inf), ("k", math.inf)])
+def test_infinities_reach_only_what_follows_them(n, at, what, value):
+    place = {"k": (at, 0, 7), "v": (at, 1, 33), "beta": (at, 1)}[what]
+    check_bad(n, 2, 1, 64, 64, [(what, place, value)], l2norm=False)
+
+
+@pytest.mark.parametrize("n", [16, 100])
+def test_several_bad_numbers(n):
+    check_bad(n, 4, 2, 128, 128, [("v", (n - 3, 0, 17), math.nan), ("v", (n // 2, 0, 18), math.inf), ("k", (n - 5, 1, 0), math.nan),
+                                  ("beta", (n // 3, 1), math.nan), ("decay", (n // 4, 1), math.nan), ("q", (0, 0, 0), math.nan)])
