@@ -204,6 +204,10 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sm100::smem_u32(dst)), "l"(src) : "memory");
 }
+// 16 bytes, or as many zeros, which arrive like a copy.
+__device__ __forceinline__ void cp_async16_or_zeros(void* dst, const void* src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src), "r"(some ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -220,20 +224,22 @@ __device__ __forceinline__ void load_rows(uint16_t* dst, const uint16_t* src, si
     }
 }
 
-// The same by one warp: a lane has a column of pieces.
+// The same by one warp: a lane has a column of pieces.  The zeros are copies
+// too: the arrival on the stage's barrier covers a lane's copies, not what it
+// stores itself.
 template <int W, int STRIDE>
 __device__ __forceinline__ void rows_async(uint16_t* dst, const uint16_t* src, size_t stride, int n_here, int lane) {
     constexpr int PC = W / 8, RP = 32 / PC;      // pieces of a row, rows of a pass
     const int row = lane / PC, c = lane % PC * 8;
     dst += row * STRIDE + c;
-    src += row * stride + c;
+    src += c;
     if (n_here == kC) {
 #pragma unroll
-        for (int i = 0; i < kC / RP; ++i) cp_async16(dst + i * RP * STRIDE, src + i * RP * stride);
+        for (int i = 0; i < kC / RP; ++i) cp_async16(dst + i * RP * STRIDE, src + (row + i * RP) * stride);
     } else {
         for (int i = 0; i < kC / RP; ++i) {
-            if (row + i * RP < n_here) cp_async16(dst + i * RP * STRIDE, src + i * RP * stride);
-            else *reinterpret_cast<uint4*>(dst + i * RP * STRIDE) = make_uint4(0, 0, 0, 0);
+            const bool some = row + i * RP < n_here;
+            cp_async16_or_zeros(dst + i * RP * STRIDE, src + (some ? row + i * RP : 0) * stride, some);
         }
     }
 }

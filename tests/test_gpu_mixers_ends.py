@@ -8,7 +8,7 @@ from latent_mixture_experts_softmax_b200 import binding as B
 from latent_mixture_experts_softmax_b200 import build, mixers
 
 import mixers_ref as R
-from test_gpu_mixers import DEV, batch_of, check_attend, delta_inputs, paged
+from test_gpu_mixers import DEV, batch_of, check_attend, check_delta, delta_inputs, paged
 
 pytestmark = pytest.mark.gpu
 
@@ -191,3 +191,15 @@ def test_infinities_reach_only_what_follows_them(n, at, what, value):
 def test_several_bad_numbers(n):
     check_bad(n, 4, 2, 128, 128, [("v", (n - 3, 0, 17), math.nan), ("v", (n // 2, 0, 18), math.inf), ("k", (n - 5, 1, 0), math.nan),
                                   ("beta", (n // 3, 1), math.nan), ("decay", (n // 4, 1), math.nan), ("q", (0, 0, 0), math.nan)])
+
+
+@pytest.mark.parametrize("DK,DV", [(64, 64), (128, 128)])
+@pytest.mark.parametrize("ns", [[17], [33, 63, 20], [95, 1, 31]])
+def test_ragged_chunks_behind_bad_rows(DK, DV, ns):
+    """What a chunk's missing rows hold is zeros, whatever stood in their place (rows of NaN, of the call before)."""
+    n = 96
+    st = mixers.DeltaStates(2, 1, DK, DV, n_states=8, l2norm=True, device=DEV)
+    bad = [x.to(DEV) * math.nan for x in delta_inputs(8 * n, 2, 1, DK, DV, 1)]
+    place = torch.arange(8, dtype=torch.int32, device=DEV)
+    st.forward(*bad, st.batch(R.starts([n] * 8).to(DEV), place, place, 8 * n, n), st.workspace(8 * n, 8, n))
+    check_delta(2, 1, DK, DV, ns, True, seed=DK, pad=3)
