@@ -327,8 +327,10 @@ LMOE_API int lmoe_route_noalloc(const lmoe_cfg* cfg, const void* x, const void* 
  * q_start[n_seqs] on belong to no sequence and are left as they were, so a
  * batch may be padded.  The lengths are read on the device: a captured
  * graph may be replayed with other lengths under the same n_seqs, n_tokens
- * and max_new.  Sequences may share pages that are only read; two rows of
- * one append that name the same place leave either one there.
+ * and max_new.  Sequences may share pages that are only read.  Where two rows
+ * of one append name the same place, it is left with codes and scales of
+ * both, mixed in any way (no harm in a page that padding writes to); other
+ * places are as without.
  *   Checked on the device, reported as LMOE_ERR_DEVICE_CHECK: a sequence
  *   with n_s < 0, n_s > max_new, rows outside [0, n_tokens), kv_len < 0 or
  *   beyond its page table is left out whole (its rows stay as they were); a

@@ -203,3 +203,36 @@ def test_ragged_chunks_behind_bad_rows(DK, DV, ns):
     place = torch.arange(8, dtype=torch.int32, device=DEV)
     st.forward(*bad, st.batch(R.starts([n] * 8).to(DEV), place, place, 8 * n, n), st.workspace(8 * n, 8, n))
     check_delta(2, 1, DK, DV, ns, True, seed=DK, pad=3)
+
+
+# ----------------------------------------------------------------------------
+# two rows at one place
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_two_rows_at_one_place_touch_nothing_else(fmt):
+    """Two sequences that share a page they write to: the place gets codes and scales of these rows (it is not said
+    which), every other place is as without."""
+    Hk, D, n = 2, 64, 9
+    cache = R.Cache(fmt, Hk, D, 16, [40, 40])
+    shared = cache.table.clone()
+    shared[1, 2] = shared[0, 2]
+    pk = paged(cache, Hk, Hk, D)
+    ws = pk.workspace()
+    x = torch.randn(2 * n, Hk, D, generator=torch.Generator().manual_seed(2)).bfloat16()
+    b = pk.batch(R.starts([n, n]).to(DEV), torch.tensor([40, 40], dtype=torch.int32, device=DEV), shared.to(DEV), 2 * n, n)
+    pk.append(x.to(DEV), x.to(DEV), b, ws)
+    assert B.lmoe_last_device_status(ws) == B.LMOE_OK
+    codes, scale = R.encode(x, fmt)
+    got_c, got_s = pk.k.float().cpu(), pk.k_scale.cpu()
+    place = shared[0, 2].item()
+    for i in range(1, n):             # positions 32 .. 39 of both
+        c, s = got_c[place, :, i - 1], got_s[place, :, i - 1]
+        assert ((c == codes[i]) | (c == codes[n + i])).all() and ((s == scale[i]) | (s == scale[n + i])).all()
+    for s in range(2):
+        cache.put("k", s, [31], x[[s * n]])
+    for page in range(cache.n_pages):
+        if page != place:
+            assert torch.equal(pk.k[page].cpu().view(torch.uint8), cache.buffers("cpu")[0][page].view(torch.uint8))
+            assert torch.equal(got_s[page].nan_to_num(-1), cache.scale["k"][page].nan_to_num(-1))
+    assert torch.equal(pk.k[place, :, n - 1:].cpu().view(torch.uint8), cache.buffers("cpu")[0][place, :, n - 1:].view(torch.uint8))
