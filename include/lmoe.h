@@ -369,9 +369,10 @@ typedef struct {
 LMOE_API int lmoe_attn_cfg_check(const lmoe_attn_cfg* cfg);
 
 /* Bytes of the workspace of lmoe_kv_append, lmoe_kv_read and lmoe_attend for
- * batches of any size (the lengths do not enter): 64 MiB and some, most of it
- * for the operands of lmoe_attend's prompt chunks.  0 if the configuration is
- * unsupported. */
+ * batches of any size (the lengths do not enter): 83 MiB for head_dim 64, 102
+ * for 128 and 256 -- 64 for the operands of lmoe_attend's prompt chunks, the
+ * rest for the parts of work that is cut between blocks.  0 if the
+ * configuration is unsupported. */
 LMOE_API size_t lmoe_attn_workspace_bytes(const lmoe_attn_cfg* cfg);
 
 /* Quantise the new tokens' keys and values into the cache.
@@ -402,8 +403,10 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  *   out  bf16 [n_tokens][n_heads][head_dim]
  *   lse  fp32 [n_tokens][n_heads] or NULL: log of the sum of exponentials
  *        (-inf for a row without keys), for joining parts of a context
- * Products are of the bf16 queries and the stored codes as fp16, exact, with
- * fp32 sums; the probabilities (times the value's scale) are rounded to
+ * Products are of the queries and the stored codes as fp16, with fp32 sums.
+ * The codes are exact, and so are a query's elements down to 2^-17 of its
+ * row's largest; smaller ones are off by up to 2^-25 of the power of two below
+ * that.  The probabilities (times the value's scale) are rounded to
  * fp16.  A value row of zeros (scale 0, or codes of zeros under the scale 1
  * that lmoe_kv_append stores) counts in the sum of exponentials and nowhere
  * else; a value scale that is no number from 0 on makes the queries that see
@@ -424,8 +427,9 @@ LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, c
  *   S <- exp(log_decay) S;  S <- S + beta k (v - k^T S);  out = scale S^T q
  * Batches with max_new up to 16 run in one launch, longer sequences in chunks
  * of 32 tokens.  The state and every sum are fp32; fp32 operands that go into
- * the state enter the products with all their bits, those that only go into
- * out with 16.  A number that is not finite leaves earlier tokens, other heads
+ * the state enter the products as three bf16 terms (all 24 bits; products of
+ * terms below 2^-24 of the whole are left out), those that only go into out as
+ * two (16 bits).  A number that is not finite leaves earlier tokens, other heads
  * and, in v, other columns as they are; it makes outputs from its token on and
  * the state NaN or infinite (in q: its token's outputs only).  Results do not
  * depend on timing. */

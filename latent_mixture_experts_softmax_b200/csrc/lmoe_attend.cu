@@ -13,7 +13,8 @@
 // fp16 whatever the scales are: p is below 2^16 (kMaxP) and the codes are
 // exact in fp16 (integers up to 127, E4M3 values), so the only rounding is
 // that of p to fp16 (half a step, 2^-11).  Queries are scaled by a power of
-// two per row into the fp16 range, which is exact; sums are fp32.
+// two per row, their largest into [1, 2): exact in fp16 down to 2^-17 of it,
+// smaller elements (fp16's subnormals) off by up to 2^-25; sums are fp32.
 //
 // What bounds it: the bytes of the codes, each read once (64 tokens of a batch
 // over up to 16K cached ones: 131 us, 4.4 TB/s), up to 8 rows; with 32 rows

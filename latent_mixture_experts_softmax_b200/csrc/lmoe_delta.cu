@@ -11,8 +11,9 @@
 // Products run on mma.sync m16n8k16 in bf16 (matrices of 16 and 32 rows are
 // too small for a tcgen05 tile): q and k are exact operands as they come.
 // What is held in fp32 and goes into the state (S in K S, T, the right-hand
-// sides, U) enters as the sum of three bf16 terms, all 24 bits; what only
-// goes into the outputs, which are bf16, as two (2^-16 of its size).  Sums
+// sides, U) enters as the sum of three bf16 terms, all 24 bits (of three terms
+// by three, the products below 2^-24 are left out); what only goes into the
+// outputs, which are bf16, as two (2^-16 of its size).  Sums
 // are fp32, and the tensor cores, which truncate where they add, never add to
 // the state itself: S exp(G_C) + delta is one rounded fma an element.  (With
 // two terms throughout, the state was 2.6e-6 of its size off after prompts of

@@ -145,6 +145,29 @@ def test_zeros_before_rows_of_other_sizes(n, group):
         attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("n,group", ROWS)
+def test_queries_with_elements_of_unequal_size(D, n, group):
+    """Elements far below their row's largest, where only these meet keys: off by 2^-25 of its power of two at most."""
+    m = n + 60
+    g = torch.Generator().manual_seed(n)
+    cache = R.Cache("int8", 1, D, 16, [m])
+    k = torch.randn(m, 1, D, generator=g) * 2.0 ** 14
+    k[:, :, 0] = 0
+    cache.put("k", 0, range(m), k.bfloat16())
+    q = torch.randn(n, group, D, generator=g) * torch.exp2(-12 - 10 * torch.rand(n, group, D, generator=g))
+    q[:, :, 0] = 1.5
+    q = q.bfloat16()
+    pk = paged(cache, group, 1, D)
+    ws = pk.workspace()
+    out = pk.attend(q.to(DEV), batch_of(pk, cache, [n]), ws)
+    K, V = cache.rows("k", 0), cache.rows("v", 0)
+    want, _, tol, _ = R.attend(q, K, V, m - n, D ** -0.5, True, 0)
+    # every weight is off by twice the largest score's error, to first order, and a little for the second
+    ds = D ** -0.5 * 2.0 ** -25 * K.abs().sum(-1).max()
+    R.assert_within(out, want, tol + 2.2 * ds * V.abs().max(), "out")
+
+
 # ----------------------------------------------------------------------------
 # the gated delta rule and numbers that are not finite
 # ----------------------------------------------------------------------------

@@ -182,3 +182,9 @@ def test_the_tensor_classes_refuse_what_does_not_fit():
         kv.attend(q, b, ws, lse=torch.zeros(3, 4, dtype=torch.float64))
     with pytest.raises(ValueError):
         kv.append(q, q, b, ws)
+
+
+def test_workspace_sizes_are_those_the_header_states(L):
+    for d, mib in ((64, 83), (128, 102), (256, 102)):
+        cfg = B.lmoe_attn_cfg(4, 2, d, 16, 0)
+        assert mib - 1 < B.lmoe_attn_workspace_bytes(cfg) / 2 ** 20 <= mib + 0.1
