@@ -13,9 +13,10 @@ liblmoe.so.
 Arguments are checked for type, shape, strides and device; what a call finds
 wrong on the device (lengths, pages, states) is read with
 `binding.lmoe_last_device_status(ws)`.  A call runs on the current stream of
-its tensors' device (or on `stream`), and a workspace serves one call at a
-time: calls on different streams, and graphs replayed side by side, need
-their own."""
+its tensors' device (or on `stream`: a stream or its handle, whose memory the
+results then are), and a workspace serves one call at a time: calls on
+different streams, and graphs replayed side by side, need their own.  A
+workspace is cleared on the stream that is current where it is made."""
 from __future__ import annotations
 
 import torch
@@ -28,6 +29,15 @@ _KV = {"int8": (B.LMOE_KV_INT8, torch.int8), "e4m3": (B.LMOE_KV_E4M3, torch.floa
 def _stream_of(device, stream):
     # (the raw handle: torch.cuda.current_stream builds an object, a third of a small call's time)
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
+
+
+def _empty(shape, device, stream):
+    """A bf16 result in the memory of the stream that writes it: memory of another may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
 
 
 def _run(device, call, *args):
@@ -144,7 +154,7 @@ class PagedKV:
         """(k, v) of the batch's tokens as bf16 values; out: a pair of tensors to write."""
         self._same_device(batch, ws)
         shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
-        k, v = out if out is not None else (torch.empty(shape, dtype=torch.bfloat16, device=self.device) for _ in "kv")
+        k, v = out if out is not None else (_empty(shape, self.device, stream) for _ in "kv")
         ks, vs = _rows(k, shape, "k", self.device), _rows(v, shape, "v", self.device)
         _run(self.device, B.lmoe_kv_read, self.cfg, self.c, batch.c, k, v, ks, vs, ws, _stream_of(self.device, stream))
         return k, v
@@ -155,7 +165,7 @@ class PagedKV:
         self._same_device(batch, ws)
         shape = (batch.n_tokens, self.n_heads, self.head_dim)
         qs = _rows(q, shape, "q", self.device)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if out is None else _whole(out, shape, torch.bfloat16, "out", self.device)
+        out = _empty(shape, self.device, stream) if out is None else _whole(out, shape, torch.bfloat16, "out", self.device)
         if lse is not None:
             _whole(lse, shape[:2], torch.float32, "lse", self.device)
         _run(self.device, B.lmoe_attend, self.cfg, self.c, batch.c, q, qs,
@@ -215,7 +225,7 @@ class DeltaStates:
         vs = _rows(v, shape, "v", d)
         for t, n in ((log_decay, "log_decay"), (beta, "beta")):
             _whole(t, shape[:2], torch.float32, n, d)
-        out = torch.empty(shape, dtype=torch.bfloat16, device=d) if out is None else _whole(out, shape, torch.bfloat16, "out", d)
+        out = _empty(shape, d, stream) if out is None else _whole(out, shape, torch.bfloat16, "out", d)
         _run(d, B.lmoe_delta_rule, self.cfg, batch.c, q, k, v, qs, ks, vs, log_decay, beta,
              self.head_k ** -0.5 if scale is None else scale, self.state, out, ws, _stream_of(d, stream))
         return out

@@ -229,6 +229,36 @@ def test_ragged_chunks_behind_bad_rows(DK, DV, ns):
 
 
 # ----------------------------------------------------------------------------
+# streams
+# ----------------------------------------------------------------------------
+
+def test_results_of_a_call_on_another_stream_are_that_streams_memory():
+    """A result allocated for the current stream may take memory that its earlier work still writes to."""
+    n = 1201
+    cache = R.Cache("int8", 8, 256, 1024, [n])
+    pk = paged(cache, 8, 8, 256)
+    ws = pk.workspace()
+    b = batch_of(pk, cache, [n])
+    st = mixers.DeltaStates(16, 16, 128, 128, n_states=1, device=DEV)
+    db = st.batch(R.starts([n]).to(DEV), *(torch.zeros(1, dtype=torch.int32, device=DEV) for _ in "sd"), n, n)
+    dws = st.workspace(n, 1, n)
+    q = torch.randn(n, 8, 256, device=DEV).bfloat16()
+    x = [t.to(DEV) for t in delta_inputs(n, 16, 16, 128, 128, 1)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        for call in (lambda: [pk.attend(q, b, ws, stream=stream)], lambda: pk.read(b, ws, stream=stream),
+                     lambda: [st.forward(*x, db, dws, stream=stream)]):
+            torch.cuda.empty_cache()
+            results = call()
+            side.synchronize()
+            at, shape = {y.data_ptr() for y in results}, results[0].shape
+            del results
+            with torch.cuda.stream(side):     # the stream's next memory of this size is what they had
+                assert torch.empty(shape, dtype=torch.bfloat16, device=DEV).data_ptr() in at
+
+
+# ----------------------------------------------------------------------------
 # two rows at one place
 # ----------------------------------------------------------------------------
 
