@@ -405,19 +405,20 @@ LMOE_API int lmoe_kv_read(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, 
  *        (-inf for a row without keys), for joining parts of a context
  * Products are of the queries and the stored codes as fp16, with fp32 sums.
  * The codes are exact, and so are a query's elements down to 2^-17 of its
- * row's largest; smaller ones are off by up to 2^-25 of the power of two below
- * that.  The probabilities (times the value's scale) are rounded to
+ * row's largest; smaller ones are off by up to 2^-25 of the power of two
+ * below that.  The probabilities (times the value's scale) are rounded to
  * fp16.  A value row of zeros (scale 0, or codes of zeros under the scale 1
  * that lmoe_kv_append stores) counts in the sum of exponentials and nowhere
  * else; a value scale that is no number from 0 on makes the queries that see
- * its row NaN.  The scales of the other value rows that one query sees may lie
- * up to 2^100 apart; those from 2^-109 (the smallest that lmoe_kv_append stores) to
- * 2^109 leave 24 bits in the sum of exponentials, larger ones 12 or more.
- * Results do not depend on timing.
+ * its row NaN.  The scales of the other value rows that one query sees may
+ * lie up to 2^100 apart; those from 2^-109 (the smallest that lmoe_kv_append
+ * stores) to 2^109 leave 24 bits in the sum of exponentials, larger ones 12
+ * or more.  softmax_scale times log2(e) and a query's largest element, or a
+ * key's scale, has to stay inside fp32.  Results do not depend on timing.
  * Errors: LMOE_ERR_ARG (also window < 0, window without causal, a scale that
- * is not finite), _UNSUPPORTED (also 2^31 - 1024 or more query rows of one
- * sequence and key head), _WORKSPACE; n_tokens = 0 or n_seqs = 0 launches
- * nothing. */
+ * is not finite, times log2(e) too), _UNSUPPORTED (also 2^31 - 1024 or more
+ * query rows of one sequence and key head), _WORKSPACE; n_tokens = 0 or
+ * n_seqs = 0 launches nothing. */
 LMOE_API int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe_kv_batch* batch, const void* q,
                          size_t q_stride, float softmax_scale, int causal, int window, void* out, float* lse, void* ws,
                          size_t ws_bytes, void* stream);

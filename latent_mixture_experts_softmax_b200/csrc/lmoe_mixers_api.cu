@@ -124,13 +124,14 @@ int lmoe_attend(const lmoe_attn_cfg* cfg, const lmoe_kv_cache* cache, const lmoe
     bool empty = false;
     const int s = kv_params(cfg, cache, batch, ws, ws_bytes, &p, &empty);
     if (s != LMOE_OK) return s;
-    if (window < 0 || (window > 0 && !causal) || !std::isfinite(softmax_scale)) return LMOE_ERR_ARG;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (window < 0 || (window > 0 && !causal) || !std::isfinite(scale_log2)) return LMOE_ERR_ARG;
     if (empty) return LMOE_OK;
     if (!rows_ok(q, q_stride, (size_t)p.Hq * p.D) || !out || !aligned(out, 16) || (lse && !aligned(lse, 4)))
         return LMOE_ERR_ARG;
     p.q = static_cast<const uint16_t*>(q);
     p.q_stride = q_stride;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.causal = causal != 0;
     // a window as wide as the cache hides nothing (and position - window stays in an int)
     p.window = window < ((long long)p.table_stride << p.page_log2) ? window : 0;

@@ -188,3 +188,12 @@ def test_workspace_sizes_are_those_the_header_states(L):
     for d, mib in ((64, 83), (128, 102), (256, 102)):
         cfg = B.lmoe_attn_cfg(4, 2, d, 16, 0)
         assert mib - 1 < B.lmoe_attn_workspace_bytes(cfg) / 2 ** 20 <= mib + 0.1
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -3.3e38])
+def test_a_softmax_scale_beyond_fp32_in_base_two_is_refused(L, scale):
+    """The kernels work in powers of two: scale * log2(e) has to be finite as well."""
+    cfg = B.lmoe_attn_cfg(4, 2, 64, 16, 0)
+    cache, batch = B.lmoe_kv_cache(256, 256, 256, 256, 8), B.lmoe_kv_batch(256, 256, 256, 2, 4, 6, 3)
+    assert L.lmoe_attend(cfg, cache, batch, 256, 256, scale, 1, 0, 256, None, 256, 1 << 40, None) == B.LMOE_ERR_ARG
+    assert L.lmoe_attend(cfg, cache, batch, 256, 256, 2.3e38, 1, 0, 256, None, 256, 0, None) == B.LMOE_ERR_WORKSPACE
