@@ -52,8 +52,8 @@ def test_a_window_wider_than_any_cache(window, Hq, Hk, D, ns, kv):
 # ----------------------------------------------------------------------------
 # the size of value rows
 # ----------------------------------------------------------------------------
-# new tokens and query heads per key head: 5 rows, 80 (converted on the way), 600 and 1200 (images)
 
+# new tokens and query heads per key head: 5 rows, 80 (converted on the way), 600 and 1200 (images)
 ROWS = [(5, 1), (40, 2), (150, 4), (300, 4)]
 
 
@@ -166,6 +166,17 @@ def test_queries_with_elements_of_unequal_size(D, n, group):
     # every weight is off by twice the largest score's error, to first order, and a little for the second
     ds = D ** -0.5 * 2.0 ** -25 * K.abs().sum(-1).max()
     R.assert_within(out, want, tol + 2.2 * ds * V.abs().max(), "out")
+
+
+# ----------------------------------------------------------------------------
+# long contexts of single tokens
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt,Hq,Hk,D,page,kv", [("int8", 5, 1, 128, 256, 9000), ("e4m3", 16, 1, 256, 1024, 6100),
+                                                ("int8", 3, 1, 64, 1024, 20000), ("e4m3", 8, 2, 128, 256, 16000)])
+def test_one_token_behind_a_long_context(fmt, Hq, Hk, D, page, kv):
+    """An item in more than 32 parts."""
+    check_attend(fmt, Hq, Hk, D, page, [1], [kv], seed=D)
 
 
 # ----------------------------------------------------------------------------
