@@ -75,6 +75,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 // accumulators to 128 registers.
 template <int D, int FMT, int NR, int NS>
 struct Few {
+    static_assert(NS == 1 || (NS == 2 && D == 256), "a lane's 16 bytes of each half of a value row");
     static constexpr int kRows = 8 * NR;
     static constexpr int kGroups = kWarps / NS;
     static constexpr int kSteps = D / 16;              // K steps of the score product
@@ -102,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
     __shared__ float s_qscale[kMaxRows];
     __shared__ int s_pos[kMaxRows];
     __shared__ float s_m[kWarps][kMaxRows], s_l[kWarps][kMaxRows];
-    __shared__ uint32_t s_any[NS == 2 ? kWarps : 1][4];
 
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -346,20 +346,23 @@ __global__ void __launch_bounds__(kThreads, Few<D, FMT, NR, NS>::kCtasPerSm)
             }
             bool z0 = false, z1 = false;                 // rows g and g + 8 are zeros
             if (__builtin_expect(zeros, 0)) {
-                // bit g * 4 + t of any[h] tells of codes in row 2 t + (h & 1) + 8 (h >> 1)
+                // bit g * 4 + t of any[h] tells of codes in row 2 t + (h & 1) + 8 (h >> 1).
+                // (The other warp's columns are read here: a barrier of the two would
+                // hang where a row behind the last token, which another call may be
+                // writing, shows one of them a scale of 1.)
                 uint32_t any[4];
+                bool here = true;
+                const uint8_t* others = NS == 2 ? p.v + locate(st, here) * D + ((hs ^ 1) * 8 + g) * 16 : nullptr;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     uint32_t w = 0;
 #pragma unroll
                     for (int i = 0; i < C::kVw; ++i) w |= vw[h][i];
+                    if (NS == 2) {
+                        const uint4 y = ldg_stream(reinterpret_cast<const uint4*>(others + (2 * t + (h & 1) + 8 * (h >> 1)) * D));
+                        w |= y.x | y.y | y.z | y.w;
+                    }
                     any[h] = __ballot_sync(0xffffffffu, (FMT == LMOE_KV_INT8 ? w : w & 0x7f7f7f7fu) != 0);
-                }
-                if (NS == 2) {       // (the other warp's columns; the next step's barrier keeps it from writing anew too early)
-                    if (lane < 4) s_any[warp][lane] = lane == 0 ? any[0] : lane == 1 ? any[1] : lane == 2 ? any[2] : any[3];
-                    named_bar_sync(1 + grp, 64);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) any[h] |= s_any[warp ^ 1][h];
                 }
                 const uint32_t row_g = 0x11111111u << (g >> 1);
                 z0 = iv0 == kNull || (iv0 == kSumUnit && !((g & 1 ? any[1] : any[0]) & row_g));

@@ -53,8 +53,8 @@ def test_a_window_wider_than_any_cache(window, Hq, Hk, D, ns, kv):
 # the size of value rows
 # ----------------------------------------------------------------------------
 
-# new tokens and query heads per key head: 5 rows, 80 (converted on the way), 600 and 1200 (images)
-ROWS = [(5, 1), (40, 2), (150, 4), (300, 4)]
+# new tokens and query heads per key head: 5, 15 and 30 rows, 80 (converted on the way), 600 and 1200 (images)
+ROWS = [(5, 1), (5, 3), (6, 5), (40, 2), (150, 4), (300, 4)]
 
 
 @pytest.mark.parametrize("fmt,D", [("int8", 128), ("e4m3", 256), ("int8", 64)])
@@ -88,14 +88,31 @@ def test_value_rows_of_zeros(fmt, D, n, group, size, zero_scale):
     assert (out[n:] == 0).all()
 
 
-@pytest.mark.parametrize("n,group", [(5, 1), (40, 2), (300, 4)])
-def test_a_scale_of_zero_makes_its_codes_zeros(n, group):
+@pytest.mark.parametrize("n,group", ROWS)
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_scale_of_zero_makes_its_codes_zeros(D, n, group):
     """value = code * scale, codes that are not zero under a scale of 0 included."""
-    cache = R.Cache("int8", 1, 64, 16, [n + 90])
+    cache = R.Cache("int8", 1, D, 16, [n + 90])
     g = torch.Generator().manual_seed(1)
     for pos in torch.randperm(n + 90, generator=g)[:30].tolist():
         cache.scale["v"][cache.table[0, pos // 16].item(), :, pos % 16] = 0.0
-    attended(cache, group, 1, 64, torch.randn(n, group, 64, generator=g).bfloat16(), [n])
+    attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
+
+
+@pytest.mark.parametrize("D,n,group", [(64, 5, 1), (256, 5, 3), (256, 6, 5), (128, 40, 2), (64, 150, 4), (256, 150, 4)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_under_a_scale_of_one(fmt, D, n, group):
+    """A cache whose scales are all 1, as formats without scales have it, a few of its rows zeros: in their first
+    bytes, in half of their columns, in all of them."""
+    cache = R.Cache(fmt, 1, D, 16, [n + 150], seed=n)
+    g = torch.Generator().manual_seed(n)
+    for name in "kv":
+        cache.scale[name][:] = 1.0
+    cache.scale["k"] *= 0.02
+    for i, pos in enumerate(torch.randperm(n + 150, generator=g)[:60].tolist()):
+        row = cache.codes["v"][cache.table[0, pos // 16].item(), 0, pos % 16]
+        row[slice(*((0, 20), (0, D // 2), (D // 2, D), (0, D))[i % 4])] = 0
+    attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
