@@ -318,6 +318,8 @@ LMOE_API int lmoe_route_noalloc(const lmoe_cfg* cfg, const void* x, const void* 
  *   row with a < 2^-100 is stored as zeros with scale 1, a row with an
  *   infinity or a NaN as zeros with a NaN scale (every query that reads it
  *   then gets NaN), which is also reported.
+ *   A cache written by other means holds no codes that are NaN in a
+ *   sequence's rows (lmoe_attend multiplies codes of masked places by 0).
  *
  * A batch describes the new tokens of n_seqs sequences: rows
  * q_start[s] .. q_start[s+1] - 1 of the token arrays are the last tokens of

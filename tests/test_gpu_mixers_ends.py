@@ -286,6 +286,102 @@ def test_results_of_a_call_on_another_stream_are_that_streams_memory():
                 assert torch.empty(shape, dtype=torch.bfloat16, device=DEV).data_ptr() in at
 
 
+@pytest.mark.parametrize("stream", [0, "default"])
+def test_the_default_stream_by_handle_and_by_object(stream):
+    cache = R.Cache("int8", 2, 64, 16, [50])
+    pk = paged(cache, 4, 2, 64)
+    ws = pk.workspace()
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    out = pk.attend(q.to(DEV), batch_of(pk, cache, [3]), ws, stream=torch.cuda.default_stream() if stream else 0)
+    want, _, tol, _ = R.attend(q, cache.rows("k", 0), cache.rows("v", 0), 47, 0.125, True, 0)
+    R.assert_within(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("n,group", [(1, 5), (6, 5), (40, 2), (150, 4)])
+def test_rows_behind_the_last_token_may_be_written_meanwhile(n, group):
+    """Attention of one step while another stream appends the next step's rows to the same pages."""
+    D, m, more = 256, 1000, 100
+    cache = R.Cache("int8", 1, D, 64, [m + more])
+    pk = paged(cache, group, 1, D)
+    wss = [pk.workspace() for _ in range(2)]
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn(n, group, D, generator=g).bfloat16()
+    dq = q.to(DEV)
+    rows = [(torch.randn(more, 1, D, generator=g) * (i % 3)).bfloat16().to(DEV) for i in range(6)]     # rows of zeros as well
+    now, after = batch_of(pk, cache, [n], lens=[m]), batch_of(pk, cache, [more])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(30):
+        with torch.cuda.stream(streams[0]):
+            got.append(pk.attend(dq, now, wss[0]))
+        with torch.cuda.stream(streams[1]):
+            for _ in range(4):
+                pk.append(rows[i % 6], rows[(i + 1) % 6], after, wss[1])
+    torch.cuda.synchronize()
+    want, _, tol, _ = R.attend(q, cache.rows("k", 0, m), cache.rows("v", 0, m), m - n, D ** -0.5, True, 0)
+    for out in got:
+        R.assert_within(out, want, tol, "out")
+    assert B.lmoe_last_device_status(wss[0]) == B.LMOE_OK and B.lmoe_last_device_status(wss[1]) == B.LMOE_OK
+
+
+# ----------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ----------------------------------------------------------------------------
+
+def test_a_cache_of_more_than_four_gigabytes():
+    Hk, D, page, pages = 2, 128, 64, 270000            # codes of 4.4 GB, keys and values each
+    small = R.Cache("int8", Hk, D, page, [700, 300])
+    at = torch.tensor([pages - 1 - i if i % 2 else i for i in range(small.n_pages)])
+    table = torch.where(small.table >= 0, at[small.table.clamp_min(0).long()].int(), small.table)
+    pk = mixers.PagedKV(8, Hk, D, page, n_pages=pages, device=DEV)
+    ws = pk.workspace()
+    for big, x in zip((pk.k, pk.v, pk.k_scale, pk.v_scale), small.buffers(DEV)):
+        big[at.to(DEV)] = x
+    g = torch.Generator().manual_seed(1)
+    for ns in ([1, 1], [4, 2], [40, 3], [200, 300]):   # (8, 16, 160 and 1200 rows: each kernel)
+        T = sum(ns)
+        b = pk.batch(R.starts(ns).to(DEV), torch.tensor(small.kv, dtype=torch.int32, device=DEV), table.to(DEV), T, max(ns))
+        x = torch.randn(T, 8 + 2 * Hk, D, generator=g).bfloat16()
+        dx = x.to(DEV)
+        pk.append(dx[:, 8:8 + Hk], dx[:, 8 + Hk:], b, ws)
+        out, back = pk.attend(dx[:, :8], b, ws), pk.read(b, ws)
+        t0 = 0
+        for s, n in enumerate(ns):
+            w = slice(t0, t0 + n)
+            for name, i in (("k", 8), ("v", 8 + Hk)):
+                small.put(name, s, range(small.kv[s] - n, small.kv[s]), x[w, i:i + Hk])
+            K, V = small.rows("k", s), small.rows("v", s)
+            for y, want in zip(back, (K, V)):
+                R.assert_within(y[w], want[small.kv[s] - n:], R.U_BF16 * want[small.kv[s] - n:].abs() * (1 + 2.0 ** -20), "read back")
+            want, _, tol, _ = R.attend(x[w, :8], K, V, small.kv[s] - n, D ** -0.5, True, 0)
+            R.assert_within(out[w], want, tol, f"out of sequence {s}")
+            t0 += n
+    assert B.lmoe_last_device_status(ws) == B.LMOE_OK
+
+
+def test_states_of_more_than_four_gigabytes():
+    H, DK, DV, places = 32, 128, 128, 2200             # 2 MB a state
+    states = torch.zeros(places, H, DK, DV, device=DEV)
+    st = mixers.DeltaStates(H, 16, DK, DV, l2norm=True, state=states)
+    for ns in ([2, 1], [40, 17]):
+        T = sum(ns)
+        x = delta_inputs(T, H, 16, DK, DV, T, l2norm=True)
+        src, dst = [places - 1, 3], [5, places - 2]
+        S = torch.randn(2, H, DK, DV, generator=torch.Generator().manual_seed(T))
+        states[src] = S.to(DEV)
+        ints = [torch.tensor(i, dtype=torch.int32, device=DEV) for i in (src, dst)]
+        out = st.forward(*(y.to(DEV) for y in x), st.batch(R.starts(ns).to(DEV), *ints, T, max(ns)), st.workspace(T, 2, max(ns)))
+        t0 = 0
+        for s, n in enumerate(ns):
+            w = slice(t0, t0 + n)
+            o, S1 = R.delta(*(y[w] for y in x), S[s], DK ** -0.5, True)
+            mag = S1.abs().amax()
+            R.assert_within(out[w], o, R.U_BF16 * 1.01 * o.abs() + 2.0 ** -14 * mag, f"out of sequence {s}")
+            R.assert_within(states[dst[s]], S1, 32 * R.U_F32 * math.sqrt(DK + n) * mag * torch.ones_like(S1), f"state {s}")
+            t0 += n
+
+
 # ----------------------------------------------------------------------------
 # two rows at one place
 # ----------------------------------------------------------------------------
