@@ -24,9 +24,10 @@
 //
 // A number that is not finite must not reach the tokens before it: the zeros
 // above T's and P's diagonals are factors of the products like any other.  So
-// where an update U is not finite, k_delta_scan cuts the right-hand sides and
-// updates off at the first token that is not, a column at a time, and makes
-// what follows it NaN; k_delta_short falls back on the recurrence.
+// where an update U is not finite, k_delta_scan makes the outputs anew from
+// right-hand sides and updates that are cut off at the first token that is not,
+// a column at a time (the column's state is lost as it should be);
+// k_delta_short falls back on the recurrence.
 //
 // k_delta_short takes a few tokens (one chunk of up to 16) in one launch,
 // bound by the state's bytes, read and written once.  (The plain recurrence,
@@ -233,14 +234,15 @@ __device__ __forceinline__ void rows_async(uint16_t* dst, const uint16_t* src, s
     constexpr int PC = W / 8, RP = 32 / PC;      // pieces of a row, rows of a pass
     const int row = lane / PC, c = lane % PC * 8;
     dst += row * STRIDE + c;
-    src += c;
+    const uint16_t* first = src;
+    src += row * stride + c;
     if (n_here == kC) {
 #pragma unroll
-        for (int i = 0; i < kC / RP; ++i) cp_async16(dst + i * RP * STRIDE, src + (row + i * RP) * stride);
+        for (int i = 0; i < kC / RP; ++i) cp_async16(dst + i * RP * STRIDE, src + i * RP * stride);
     } else {
         for (int i = 0; i < kC / RP; ++i) {
             const bool some = row + i * RP < n_here;
-            cp_async16_or_zeros(dst + i * RP * STRIDE, src + (some ? row + i * RP : 0) * stride, some);
+            cp_async16_or_zeros(dst + i * RP * STRIDE, some ? src + i * RP * stride : first, some);
         }
     }
 }
@@ -795,6 +797,60 @@ constexpr uint64_t kWaitLimit = 4000000000ull;   // SM cycles per barrier wait (
 constexpr int kN = 32;                       // state columns of a block
 constexpr int kStages = 3;
 
+// (P U)^T of a chunk's tokens 16 hf .. 16 hf + 15 from updates that are not all
+// finite: right-hand sides and updates are cut off at each column's first token
+// that is not.
+struct Rhs {
+    float y[4][4];
+};
+struct Outputs {
+    float o[2][4];
+};
+__device__ __forceinline__ void times_p(float (&o)[2][4], const float (&u)[4][4], const ChunkData& d, int hf, int lane) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k > hf) continue;
+        uint32_t hi[4], lo[4];
+        split_a(u[2 * k], u[2 * k + 1], hi, lo);
+        uint4 f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f[j] = d.p[k ? 4 + j : 2 * hf + j][lane];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].x, f[j].y);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].z, f[j].w);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mma_bf16(o[j], lo, f[j].x, f[j].y);
+    }
+}
+__device__ __noinline__ Outputs outputs_cut_off(Rhs r, const ChunkData& d, int hf, int lane) {
+    const int t = lane & 3;
+    Outputs x;
+    float u[4][4];
+    int2 cut = first_bad(r.y, t, make_int2(kC, kC));
+    cut_off(r.y, t, cut, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t a[3][4];
+        split_a(r.y[2 * k], r.y[2 * k + 1], a);
+#pragma unroll
+        for (int j = 2 * k; j < 4; ++j) mul3(u[j], a, d.t[k ? j + 2 : j][lane], d.tl[k ? j + 2 : j][lane]);
+    }
+    cut = first_bad(u, t, cut);              // (rows of T from there on; sums that overflowed)
+    cut_off(u, t, cut, 0.f);
+    times_p(x.o, u, d, hf, lane);
+    cut_off(x.o, t, make_int2(cut.x - 16 * hf, cut.y - 16 * hf), __int_as_float(0x7fffffff));
+    return x;
+}
+
 template <int DK>
 struct Scan {
     struct Stage {
@@ -972,47 +1028,34 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
         }
         // ---- U^T
         float u[4][4];
-        int2 cut = make_int2(kC, kC);            // the columns' first tokens that are not finite
-#pragma unroll 1
-        for (bool again = false;; again = true) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
+            for (int i = 0; i < 4; ++i) u[j][i] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t a[3][4];
-                split_a(ks[2 * k], ks[2 * k + 1], a);
-                const uint4* f = ft + 2 * k;
-                uint2 l[4];
+        for (int k = 0; k < 2; ++k) {
+            uint32_t a[3][4];
+            split_a(ks[2 * k], ks[2 * k + 1], a);
+            const uint4* f = ft + 2 * k;
+            uint2 l[4];
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) l[j] = x.d.tl[k ? j + 2 : j][lane];
-                // (mul3, of up to four tiles side by side)
+            for (int j = 2 * k; j < 4; ++j) l[j] = x.d.tl[k ? j + 2 : j][lane];
+            // (mul3, of up to four tiles side by side)
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[2], f[j].x, f[j].y);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[2], f[j].x, f[j].y);
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].z, f[j].w);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].z, f[j].w);
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], l[j].x, l[j].y);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], l[j].x, l[j].y);
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].x, f[j].y);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[1], f[j].x, f[j].y);
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].z, f[j].w);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].z, f[j].w);
 #pragma unroll
-                for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].x, f[j].y);
-            }
-            if (__builtin_expect(!__any_sync(0xffffffffu, not_finite(u)), 1)) break;
-            if (again) {                         // (rows of T from there on; sums that overflowed)
-                cut = first_bad(u, t, cut);
-                cut_off(u, t, cut, 0.f);
-                break;
-            }
-            cut = first_bad(ks, t, cut);
-            cut_off(ks, t, cut, 0.f);
+            for (int j = 2 * k; j < 4; ++j) mma_bf16(u[j], a[0], f[j].x, f[j].y);
         }
         // ---- the state
-        const float last = x.d.last[0], last0 = cut.x < kC ? __int_as_float(0x7fffffff) : last,
-                    last1 = cut.y < kC ? __int_as_float(0x7fffffff) : last;
+        const float last = x.d.last[0];
         uint32_t w[2][3][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -1049,28 +1092,30 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_delta_scan(DeltaParams p, i
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) S[j0 + j][i] = fmaf(S[j0 + j][i], i < 2 ? last0 : last1, d[j][i]);
+                for (int i = 0; i < 4; ++i) S[j0 + j][i] = fmaf(S[j0 + j][i], last, d[j][i]);
         }
         // ---- out^T of 16 tokens
+        float pu[2][4];
+        times_p(pu, u, x.d, hf, lane);
+        if (__builtin_expect(__any_sync(0xffffffffu, not_finite(u)), 0)) {
+            // (the state is NaN in these columns, as it has to be; outputs before are not)
+            Rhs r;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k > hf) continue;
-            uint32_t hi[4], lo[4];
-            split_a(u[2 * k], u[2 * k + 1], hi, lo);
-            uint4 f[2];
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) f[j] = x.d.p[k ? 4 + j : 2 * hf + j][lane];
+                for (int i = 0; i < 4; ++i) r.y[j][i] = ks[j][i];
+            const Outputs y = outputs_cut_off(r, x.d, hf, lane);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].x, f[j].y);
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) mma_bf16(o[j], hi, f[j].z, f[j].w);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mma_bf16(o[j], lo, f[j].x, f[j].y);
+                for (int i = 0; i < 4; ++i) pu[j][i] = y.o[j][i];      // (NaN from there on)
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][i] += pu[j][i];
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&sm.empty[st]);
-        if (__builtin_expect(__any_sync(0xffffffffu, min(cut.x, cut.y) < kC), 0))
-            cut_off(o, t, make_int2(cut.x - 16 * hf, cut.y - 16 * hf), __int_as_float(0x7fffffff));
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
