@@ -612,9 +612,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(AttendParams p, in
         float f[RW];
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
-            const float h = ex2(0.5f * (q[rr[i]] - (m[i] == -INFINITY ? 0.f : m[i])));
-            f[i] = k0 + lane < np ? h * h : 0.f;
-            const float y = twice(q[rows + rr[i]], h);
+            const float d = q[rr[i]] - (m[i] == -INFINITY ? 0.f : m[i]);
+            f[i] = k0 + lane < np ? ex2(d) : 0.f;
+            const float y = twice(q[rows + rr[i]], ex2(0.5f * d));
             l[i] = k0 + lane < np ? l[i] + y : l[i];
         }
         const int n = min(32, np - k0);

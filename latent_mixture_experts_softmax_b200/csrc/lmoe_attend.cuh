@@ -284,7 +284,7 @@ __host__ __device__ constexpr int many_rows(int D) { return D == 256 ? 128 : 256
 // Images of key tiles: tokens of a tile, bytes (keys and values in fp16, three
 // floats and a bit a token), and what a workspace holds of them: half of L2.
 __host__ __device__ constexpr int image_tokens(int) { return 64; }
-__host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12) + 16; }
+__host__ __device__ constexpr size_t image_bytes(int D) { return (size_t)image_tokens(D) * (4 * D + 12) + 128; }
 constexpr size_t kImageBytes = 64u << 20;
 // Images are made for more row tiles than kImageRowTiles, and for two to four
 // where the contexts are brief and one group takes all (300 rows over 8000
