@@ -17,9 +17,9 @@
 // smaller elements (fp16's subnormals) off by up to 2^-25; sums are fp32.
 //
 // What bounds it: the bytes of the codes, each read once (64 tokens of a batch
-// over up to 16K cached ones: 131 us, 4.4 TB/s), up to 8 rows; with 32 rows
+// over up to 16K cached ones: 130 us, 4.5 TB/s), up to 8 rows; with 32 rows
 // and head_dim 256 the latency of one block of eight warps an SM (32 tokens
-// over up to 128K: 258 us, 2.4 TB/s).  The products run
+// over up to 128K: 267 us, 2.4 TB/s).  The products run
 // on mma.sync m16n8k16 with the tokens as M (S^T = K Q^T) and the query rows
 // as N, so 8 rows cost one instruction per 16 tokens and 16 columns, and
 // neither product needs a transposed copy of the codes: both sums run over
@@ -694,6 +694,10 @@ cudaError_t launch_few(const AttendParams& p, cudaStream_t st) {
     return launch_join(p, C::kRows, kCtas, true, st);
 }
 
+// Rows of a sequence and key head, by their bound.  30 rows of head_dim 128 over
+// 8 x 4096 (4 x 32768) tokens take 57 (98) us here, 66 (162) in the kernel for
+// many rows; 65 rows 82 (186) against 66 (162).  Of 40 rows, two row tiles here
+// would take 64 (137) against 66 (162): the switch stands at one tile.
 template <int D, int FMT>
 cudaError_t launch_rows(const AttendParams& p, cudaStream_t st) {
     const long long rows = (long long)p.max_new * p.G;

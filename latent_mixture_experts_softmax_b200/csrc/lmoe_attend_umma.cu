@@ -9,7 +9,7 @@
 // the exponential unit), 300 for votes and the rare change of the reference,
 // and the rest waits for barriers; the tensor core needs 1024, at the pace at
 // which shared memory gives it Q, K and V.  4096 causal tokens of 20 heads take
-// 154 us (557 TFLOP/s), 2048 tokens over 32768 of head_dim 256 712 us (935
+// 156 us (550 TFLOP/s), 2048 tokens over 32768 of head_dim 256 713 us (934
 // TFLOP/s; the card runs that power-capped).
 //
 // A CTA (one per SM) holds query tiles of 128 rows as fp16 in shared memory
@@ -923,7 +923,8 @@ cudaError_t launch(const AttendParams& p, cudaStream_t st) {
 // Images pay where several row tiles read a key tile, and go in groups of
 // sequences, or of heads of one sequence, that fit the workspace (and L2).  A
 // sequence that may be too long for them, even one head of it, is converted
-// on the way.
+// on the way.  The lengths are on the device, so this goes by the page table's
+// width: 248,512 tokens for head_dim 64, 127,552 for 128, 64,640 for 256.
 template <int D, int FMT>
 cudaError_t launch_groups(AttendParams p, cudaStream_t st) {
     const long long tiles = (((long long)p.table_stride << p.page_log2) + image_tokens(D) - 1) / image_tokens(D);

@@ -36,7 +36,7 @@
 // and took 28 us for four tokens of 16 sequences and 32 heads, 67 MB of
 // states; this takes 25.)
 // For longer sequences k_delta_chunks makes T, P and the factors of every
-// chunk of 32, and k_delta_scan walks a sequence's chunks with S: 256 us for
+// chunk of 32, and k_delta_scan walks a sequence's chunks with S: 267 us for
 // one prompt of 4096 tokens, 32 heads of 128 x 128.
 
 #include "lmoe_mixers.cuh"
@@ -867,7 +867,7 @@ struct Scan {
 // state's rows each, in fp32 registers from the first chunk to the last; they
 // add up their shares of K S and Q S through shared memory, both compute U,
 // and each updates its rows of S and writes half of the tokens.  The chain of
-// a chunk's steps bounds it (3300 cycles, of which its 180 products take 1440;
+// a chunk's steps bounds it (3500 cycles, of which its 180 products take 1440;
 // 4700 with two blocks on an SM), so all that is not on it is done by the
 // fifth warp, which keeps two chunks ahead.
 template <int DK>
