@@ -99,6 +99,29 @@ def test_a_scale_of_zero_makes_its_codes_zeros(D, n, group):
     attended(cache, group, 1, D, torch.randn(n, group, D, generator=g).bfloat16(), [n])
 
 
+@pytest.mark.parametrize("bad", [-1.0, -0.03, math.inf, math.nan])
+@pytest.mark.parametrize("codes", ["any", "zeros"])
+@pytest.mark.parametrize("D,n,group", [(64, 6, 1), (256, 6, 5), (128, 40, 2), (64, 150, 4)])
+def test_a_value_scale_that_is_no_number_from_zero_on_reaches_only_the_queries_that_see_it(bad, codes, D, n, group):
+    m = n + 90
+    cache = R.Cache("int8", 1, D, 16, [m], seed=n)
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn(n, group, D, generator=g).bfloat16()
+    at = m - n // 2
+    page = cache.table[0, at // 16].item()
+    if codes == "zeros":
+        cache.codes["v"][page, :, at % 16] = 0.0
+    K, V = cache.rows("k", 0), cache.rows("v", 0)
+    cache.scale["v"][page, :, at % 16] = bad
+    pk = paged(cache, group, 1, D)
+    ws = pk.workspace()
+    out = pk.attend(q.to(DEV), batch_of(pk, cache, [n]), ws)
+    first = at - (m - n)                                 # the first query that sees it
+    want, _, tol, _ = R.attend(q[:first], K[:at], V[:at], m - n, D ** -0.5, True, 0)
+    R.assert_within(out[:first], want, tol, "queries before")
+    assert torch.isnan(out[first:]).all()
+
+
 @pytest.mark.parametrize("D,n,group", [(64, 5, 1), (256, 5, 3), (256, 6, 5), (128, 40, 2), (64, 150, 4), (256, 150, 4)])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 def test_rows_under_a_scale_of_one(fmt, D, n, group):
