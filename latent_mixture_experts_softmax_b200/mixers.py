@@ -26,9 +26,14 @@ from . import binding as B
 _KV = {"int8": (B.LMOE_KV_INT8, torch.int8), "e4m3": (B.LMOE_KV_E4M3, torch.float8_e4m3fn)}
 
 
+# The current stream's handle and the current device, by torch's own short ways where it has them
+# (torch.cuda.current_stream builds an object, a third of a small call's time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_of(device, stream):
-    # (the raw handle: torch.cuda.current_stream builds an object, a third of a small call's time)
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
+    return _raw_stream(device.index) if stream is None else stream
 
 
 def _empty(shape, device, stream):
@@ -42,7 +47,7 @@ def _empty(shape, device, stream):
 
 def _run(device, call, *args):
     """One call with its tensors' device current."""
-    now = torch._C._cuda_getDevice()
+    now = _current_device()
     if now == device.index:
         return call(*args)
     torch.cuda.set_device(device)

@@ -1,4 +1,5 @@
 """The token mixers at the ends of what their calls accept, on the GPU, against the 64-bit forms of tests/mixers_ref.py."""
+import importlib.util
 import math
 
 import pytest
@@ -318,6 +319,25 @@ def test_the_default_stream_by_handle_and_by_object(stream):
     out = pk.attend(q.to(DEV), batch_of(pk, cache, [3]), ws, stream=torch.cuda.default_stream() if stream else 0)
     want, _, tol, _ = R.attend(q, cache.rows("k", 0), cache.rows("v", 0), 47, 0.125, True, 0)
     R.assert_within(out, want, tol, "out")
+
+
+def test_a_torch_without_the_short_ways_to_stream_and_device(monkeypatch):
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.find_spec(mixers.__name__)
+    plain = importlib.util.module_from_spec(spec)        # (a copy of its own; the loaded module stays as it is)
+    spec.loader.exec_module(plain)
+    monkeypatch.undo()
+    cache = R.Cache("int8", 2, 64, 16, [50])
+    pk = plain.PagedKV(4, 2, 64, 16, buffers=cache.buffers(DEV))
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    side = torch.cuda.Stream()
+    want, _, tol, _ = R.attend(q, cache.rows("k", 0), cache.rows("v", 0), 47, 0.125, True, 0)
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            out = pk.attend(q.to(DEV), batch_of(pk, cache, [3]), pk.workspace())
+        stream.synchronize()
+        R.assert_within(out, want, tol, "out")
 
 
 @pytest.mark.parametrize("n,group", [(1, 5), (6, 5), (40, 2), (150, 4)])
